@@ -353,6 +353,107 @@ int qlora_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M,
                     size_t ws_bytes, void* stream);
 
 /*
+ * A pool of LoRA adapters beside one frozen weight: a batch whose rows use
+ * different adapters (requests of many users on one base model; several
+ * adapters trained side by side). The update of each row is the one of
+ * qlora_nf4_lora_fwd / _bwd_dx / qlora_lora_grad ("QLoRA and Quantized
+ * Training", "In code"; figure 2 of "A 65B fine-tune on the GPU you already
+ * have": a small adapter beside a frozen base that all of them share).
+ *   A       [n, r, K] bf16, B [n, N, r] bf16 -- the pool, 1 <= n <=
+ *           QLORA_MAX_ADAPTERS, one rank 1 <= r <= 128 (adapters of smaller
+ *           rank are padded with zeros).
+ *   scale   [n] fp32 (device): s_a = alpha / r of each adapter.
+ *   index   [M] int32 (device): the adapter of each row. Any value outside
+ *           0 .. n - 1 (-1, say) means none: the row takes the base alone and
+ *           adds to no gradient. Rows of one adapter need not be neighbours;
+ *           neighbours are faster.
+ * A NaN or infinity in one adapter, its scale or a row reaches only the rows
+ * (or the gradients) that use it. Every pointer is 16-byte aligned except scale
+ * and index (4 bytes). M < 2^31; sizes otherwise as in qlora_nf4_lora_fwd.
+ *
+ * qlora_nf4_lora_fwd_multi:  y_m  = bf16( x_m . W'^T + s_a . t_m . B_a^T ),
+ *                            t_m  = bf16(x_m . A_a^T),  a = index[m]
+ * qlora_nf4_bwd_dx_multi:    dX_m = bf16( dY_m . W' + s_a . u_m . A_a ),
+ *                            u_m  = bf16(dY_m . B_a);  N a multiple of 8
+ * qlora_lora_grad_multi:     dB_a = s_a sum_m dY_m^T (x_m . A_a^T)   [n, N, r]
+ *                            dA_a = s_a sum_m (dY_m . B_a)^T x_m     [n, r, K]
+ *     over the rows m of adapter a, fp32; t and u enter as three bf16 numbers
+ *     each, so nothing is rounded below fp32 on the way. accumulate = 0
+ *     overwrites dA and dB (zeros for an adapter without rows), 1 adds to them.
+ *     x is bf16 (xfmt = QLORA_ACT_BF16, xabsmax NULL) or an 8-bit checkpoint of
+ *     the layer input (below): its codes, format and block constants.
+ * workspace: at least qlora_workspace_bytes_multi(op, M, N, K, r, n) bytes with
+ * op = 0, 1, 2 for the three calls, with the zero-counter rule of every
+ * workspace.
+ */
+#define QLORA_MAX_ADAPTERS 4096
+int qlora_nf4_lora_fwd_multi(const uint16_t* x, int64_t M, int64_t N,
+                             int64_t K, const uint8_t* packed,
+                             const int8_t* qscale, const float* step,
+                             const uint16_t* A, const uint16_t* B,
+                             const float* scale, int n, const int32_t* index,
+                             int r, uint16_t* y, void* workspace,
+                             size_t ws_bytes, void* stream);
+int qlora_nf4_bwd_dx_multi(const uint16_t* dy, int64_t M, int64_t N,
+                           int64_t K, const uint8_t* packed,
+                           const int8_t* qscale, const float* step,
+                           const uint16_t* A, const uint16_t* B,
+                           const float* scale, int n, const int32_t* index,
+                           int r, uint16_t* dx, void* workspace,
+                           size_t ws_bytes, void* stream);
+int qlora_lora_grad_multi(const void* x, int xfmt, const uint16_t* xabsmax,
+                          const uint16_t* dy, int64_t M, int64_t N, int64_t K,
+                          const uint16_t* A, const uint16_t* B,
+                          const float* scale, int n, const int32_t* index,
+                          int r, float* dA, float* dB, int accumulate,
+                          void* workspace, size_t ws_bytes, void* stream);
+size_t qlora_workspace_bytes_multi(int op, int64_t M, int64_t N, int64_t K,
+                                   int r, int n);
+
+/*
+ * 8-bit activation checkpoints: a layer input kept between the forward and
+ * the backward pass as one byte a value and one constant per block of 64
+ * (8.25 bits a value instead of 16). With the weights in 4 bits and optimizer
+ * state for the adapters alone, the kept activations are what is left of a
+ * step's memory ("A 65B fine-tune on the GPU you already have", figure 1;
+ * "QLoRA Explained", "What is QLoRA?").
+ *   x       [numel] bf16, numel > 0 a multiple of 64 (a layer input [M, K], K a
+ *           multiple of 64, in row-major order).
+ *   fmt     QLORA_ACT_INT8: code = rne(127 x / top), signed bytes;
+ *           QLORA_ACT_E4M3: code = the OCP e4m3 value nearest 448 x / top, as
+ *           its bits. Ties to even; both quotients exact (every code is the one
+ *           that exact arithmetic gives).
+ *   absmax  [numel/64] bf16: top = max |x| of the block, exactly. A block that
+ *           holds a NaN or an infinity has NaN there and restores to all NaN;
+ *           one whose largest magnitude is below 2^-80 has 0 and restores to
+ *           zeros.
+ *   out     [numel] bf16: bf16_rne(fp32(code . s)), s = fp32(top / 127) or
+ *           fp32(top / 448).
+ * x, codes and out are 16-byte aligned.
+ */
+#define QLORA_ACT_INT8 0
+#define QLORA_ACT_E4M3 1
+#define QLORA_ACT_BF16 2     /* not a checkpoint: x itself (qlora_lora_grad_multi) */
+int qlora_act8_pack(const uint16_t* x, int64_t numel, int fmt, uint8_t* codes,
+                    uint16_t* absmax, void* stream);
+int qlora_act8_unpack(const uint8_t* codes, const uint16_t* absmax,
+                      int64_t numel, int fmt, uint16_t* out, void* stream);
+
+/*
+ * The adapter gradients of qlora_lora_grad with the layer input taken from its
+ * 8-bit checkpoint (codes and absmax [M, K], [M, K/64] of qlora_act8_pack, read
+ * as they are: nothing is restored to memory):
+ *     dB = (alpha / r) dY^T (x^ . A^T),  dA = (alpha / r) (dY . B)^T x^
+ * with x^ the restored bf16 values; t and u as in qlora_lora_grad_multi.
+ * workspace: at least qlora_workspace_bytes_multi(3, M, N, K, r, 1) bytes.
+ */
+int qlora_lora_grad_act8(const uint8_t* codes, const uint16_t* absmax, int fmt,
+                         const uint16_t* dy, int64_t M, int64_t N, int64_t K,
+                         const uint16_t* A, const uint16_t* B, int r,
+                         float alpha, float* dA, float* dB, int accumulate,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Other 16-level block formats, for comparison with NF4 ("QLoRA Explained",
  * "The three ideas behind QLoRA": NF4 beats the standard 4-bit integer and
  * float formats on normally distributed weights; figure 3 of "A 65B

@@ -19,10 +19,12 @@ Modules:
               double quantization of the constants, dequantization to bf16.
   gemm     -- forward y = x.deq(W)^T + (alpha/r).(x.A^T).B^T and
               backward dX = dY.deq(W) [+ LoRA term], in fp64.
+  multi    -- the same row by row over a pool of adapters, and 8-bit activation
+              checkpoints.
   storage  -- bits/parameter and memory arithmetic from buffer byte counts.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 (closed forms, brute force, invariants, the pages' printed figures); none is
 "parity unpinned".
 """
-from . import nf4, gemm, storage  # noqa: F401
+from . import nf4, gemm, multi, storage  # noqa: F401

@@ -45,6 +45,17 @@ SIGNATURES = [
     ("qlora_nf4_merge", _i32, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _vp]),
     ("qlora_lora_grad", _i32, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _vp, _i32,
                                _vp, _sz, _vp]),
+    ("qlora_nf4_lora_fwd_multi", _i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32,
+                                        _vp, _vp, _sz, _vp]),
+    ("qlora_nf4_bwd_dx_multi", _i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32,
+                                      _vp, _vp, _sz, _vp]),
+    ("qlora_lora_grad_multi", _i32, [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _i32,
+                                     _vp, _vp, _i32, _vp, _sz, _vp]),
+    ("qlora_workspace_bytes_multi", _sz, [_i32, _i64, _i64, _i64, _i32, _i32]),
+    ("qlora_act8_pack", _i32, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    ("qlora_act8_unpack", _i32, [_vp, _vp, _i64, _i32, _vp, _vp]),
+    ("qlora_lora_grad_act8", _i32, [_vp, _vp, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _vp, _i32,
+                                    _vp, _sz, _vp]),
     ("qlora_nf4_codebook", _i32, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     ("qlora_status_string", ctypes.c_char_p, [_i32]),
     ("qlora_last_hip_error", _i32, []),

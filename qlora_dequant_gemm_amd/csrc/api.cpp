@@ -388,4 +388,134 @@ int qlora_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M, int64_t N,
                                            as_stream(stream)));
 }
 
+// ---------------------------------------------------------------------------
+// a pool of adapters; 8-bit activation checkpoints
+// ---------------------------------------------------------------------------
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_pool(const uint16_t* A, const uint16_t* B, const float* scale, int n, const int32_t* index, int r) {
+  if (r < 1 || r > QLORA_MAX_RANK) return QLORA_ERR_RANK;
+  if (n < 1 || n > QLORA_MAX_ADAPTERS) return QLORA_ERR_SHAPE;
+  if (!A || !B || !scale || !index) return QLORA_ERR_NULL;
+  if (!aligned16(A) || !aligned16(B) || !aligned4(scale) || !aligned4(index)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+// rows are numbered with 32 bits in the lists of the gradients and in the
+// grids of the down-projections
+int check_mm_multi(int64_t M, int64_t N, int64_t K, bool rows_of_8) {
+  const int st = check_mm(M, N, K);
+  if (st) return st;
+  if (M >= (int64_t{1} << 31) || (rows_of_8 && N % 8 != 0)) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+}  // namespace
+
+size_t qlora_workspace_bytes_multi(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
+  if (op < 0 || op > 3 || r < 1 || r > QLORA_MAX_RANK || n < 1 || n > QLORA_MAX_ADAPTERS) return 0;
+  if (check_mm_multi(M, N, K, op != 0)) return 0;
+  if (op == 3) return qnf4::multi_grad_plan(M, N, K, r, 1, false).total;
+  return qnf4::multi_ws_bytes(op, M, N, K, r, n);
+}
+
+int qlora_nf4_lora_fwd_multi(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                             const float* scale, int n, const int32_t* index, int r, uint16_t* y, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (!x || !y) return QLORA_ERR_NULL;
+  int st = check_weight(packed, qscale, step);
+  if (st) return st;
+  st = check_mm_multi(M, N, K, false);
+  if (st) return st;
+  st = check_pool(A, B, scale, n, index, r);
+  if (st) return st;
+  if (!aligned16(x) || !aligned16(y)) return QLORA_ERR_ALIGN;
+  st = check_ws(workspace, ws_bytes, qnf4::multi_ws_bytes(0, M, N, K, r, n));
+  if (st) return st;
+  const qnf4::Codebook* cb = qnf4::codebook();
+  if (!cb) return QLORA_ERR_INIT;
+  return hip_status(qnf4::launch_multi_fwd(x, M, N, K, packed, qscale, step, A, B, qnf4::MultiLora{index, scale, n}, r,
+                                           y, workspace, *cb, as_stream(stream)));
+}
+
+int qlora_nf4_bwd_dx_multi(const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                           const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                           const float* scale, int n, const int32_t* index, int r, uint16_t* dx, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  if (!dy || !dx) return QLORA_ERR_NULL;
+  int st = check_weight(packed, qscale, step);
+  if (st) return st;
+  st = check_mm_multi(M, N, K, true);
+  if (st) return st;
+  st = check_pool(A, B, scale, n, index, r);
+  if (st) return st;
+  if (!aligned16(dy) || !aligned16(dx)) return QLORA_ERR_ALIGN;
+  st = check_ws(workspace, ws_bytes, qnf4::multi_ws_bytes(1, M, N, K, r, n));
+  if (st) return st;
+  const qnf4::Codebook* cb = qnf4::codebook();
+  if (!cb) return QLORA_ERR_INIT;
+  return hip_status(qnf4::launch_multi_bwd(dy, M, N, K, packed, qscale, step, A, B, qnf4::MultiLora{index, scale, n}, r,
+                                           dx, workspace, *cb, as_stream(stream)));
+}
+
+int qlora_lora_grad_multi(const void* x, int xfmt, const uint16_t* xabsmax, const uint16_t* dy, int64_t M, int64_t N,
+                          int64_t K, const uint16_t* A, const uint16_t* B, const float* scale, int n,
+                          const int32_t* index, int r, float* dA, float* dB, int accumulate, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  if (!x || !dy || !dA || !dB) return QLORA_ERR_NULL;
+  if (xfmt != QLORA_ACT_INT8 && xfmt != QLORA_ACT_E4M3 && xfmt != QLORA_ACT_BF16) return QLORA_ERR_DTYPE;
+  if ((xfmt == QLORA_ACT_BF16) != (xabsmax == nullptr)) return xabsmax ? QLORA_ERR_DTYPE : QLORA_ERR_NULL;
+  int st = check_mm_multi(M, N, K, true);
+  if (st) return st;
+  if (accumulate != 0 && accumulate != 1) return QLORA_ERR_SHAPE;
+  st = check_pool(A, B, scale, n, index, r);
+  if (st) return st;
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(dA) || !aligned16(dB) || (xabsmax && !aligned16(xabsmax)))
+    return QLORA_ERR_ALIGN;
+  st = check_ws(workspace, ws_bytes, qnf4::multi_ws_bytes(2, M, N, K, r, n));
+  if (st) return st;
+  return hip_status(qnf4::launch_multi_grad(x, xabsmax, xfmt, dy, M, N, K, A, B, scale, 0.0f, n, index, r, dA, dB,
+                                            accumulate, workspace, as_stream(stream)));
+}
+
+int qlora_lora_grad_act8(const uint8_t* codes, const uint16_t* absmax, int fmt, const uint16_t* dy, int64_t M,
+                         int64_t N, int64_t K, const uint16_t* A, const uint16_t* B, int r, float alpha, float* dA,
+                         float* dB, int accumulate, void* workspace, size_t ws_bytes, void* stream) {
+  if (!codes || !absmax || !dy || !dA || !dB) return QLORA_ERR_NULL;
+  if (fmt != QLORA_ACT_INT8 && fmt != QLORA_ACT_E4M3) return QLORA_ERR_DTYPE;
+  int st = check_mm_multi(M, N, K, true);
+  if (st) return st;
+  if (accumulate != 0 && accumulate != 1) return QLORA_ERR_SHAPE;
+  if (r < 1) return QLORA_ERR_RANK;
+  st = check_adapter(A, B, r);
+  if (st) return st;
+  if (!aligned16(codes) || !aligned16(absmax) || !aligned16(dy) || !aligned16(dA) || !aligned16(dB))
+    return QLORA_ERR_ALIGN;
+  st = check_ws(workspace, ws_bytes, qnf4::multi_grad_plan(M, N, K, r, 1, false).total);
+  if (st) return st;
+  return hip_status(qnf4::launch_multi_grad(codes, absmax, fmt, dy, M, N, K, A, B, nullptr,
+                                            alpha / static_cast<float>(r), 1, nullptr, r, dA, dB, accumulate, workspace,
+                                            as_stream(stream)));
+}
+
+int qlora_act8_pack(const uint16_t* x, int64_t numel, int fmt, uint8_t* codes, uint16_t* absmax, void* stream) {
+  if (!x || !codes || !absmax) return QLORA_ERR_NULL;
+  if (fmt != QLORA_ACT_INT8 && fmt != QLORA_ACT_E4M3) return QLORA_ERR_DTYPE;
+  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel / 8 / 256 >= (int64_t{1} << 31)) return QLORA_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(absmax)) return QLORA_ERR_ALIGN;
+  return hip_status(qnf4::launch_act8_pack(x, numel, fmt, codes, absmax, as_stream(stream)));
+}
+
+int qlora_act8_unpack(const uint8_t* codes, const uint16_t* absmax, int64_t numel, int fmt, uint16_t* out,
+                      void* stream) {
+  if (!codes || !absmax || !out) return QLORA_ERR_NULL;
+  if (fmt != QLORA_ACT_INT8 && fmt != QLORA_ACT_E4M3) return QLORA_ERR_DTYPE;
+  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel / 8 / 256 >= (int64_t{1} << 31)) return QLORA_ERR_SHAPE;
+  if (!aligned16(codes) || !aligned16(absmax) || !aligned16(out)) return QLORA_ERR_ALIGN;
+  return hip_status(qnf4::launch_act8_unpack(codes, absmax, numel, fmt, out, as_stream(stream)));
+}
+
 }  // extern "C"

@@ -50,6 +50,59 @@ __device__ __forceinline__ void tile_of(int pid, int ntm, int ntn, int& tm, int&
   tn = within / gsz;
 }
 
+// The adapters among the 256 rows of a tile, one after another in the order
+// of their first rows: next() gives an adapter and the rows that use it (row
+// 64 q + b is bit b of rows[q]), wave-uniform and the same in every wave.
+struct TileAdapters {
+  int id[4];
+  uint64_t pend[4];
+  __device__ __forceinline__ void init(const MultiLora& ml, int64_t m0, int64_t M, int lane) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t m = m0 + 64 * q + lane;
+      id[q] = m < M ? ml.index[m] : -1;
+      if (static_cast<unsigned>(id[q]) >= static_cast<unsigned>(ml.n)) id[q] = -1;
+      pend[q] = __ballot(id[q] >= 0);
+    }
+  }
+  // leave out the rows outside [32 i0, 32 (i0 + count))
+  __device__ __forceinline__ void keep(int i0, int count) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < i0 || i >= i0 + count) pend[i >> 1] &= ~(0xFFFFFFFFull << (32 * (i & 1)));
+  }
+  __device__ __forceinline__ bool next(int& a, uint64_t (&rows)[4]) {
+    if (!(pend[0] | pend[1] | pend[2] | pend[3])) return false;
+    a = pend[0]   ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pend[0]))
+        : pend[1] ? __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pend[1]))
+        : pend[2] ? __builtin_amdgcn_readlane(id[2], __builtin_ctzll(pend[2]))
+                  : __builtin_amdgcn_readlane(id[3], __builtin_ctzll(pend[3]));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      rows[q] = __ballot(id[q] == a);
+      pend[q] &= ~rows[q];
+    }
+    return true;
+  }
+};
+
+// acc += s * tmp on the rows of a 32 x 32 block that `rm` names (bit = row).
+// A row that is not named keeps its bits whatever tmp holds there: a NaN in
+// one adapter must not reach the rows of another.
+__device__ __forceinline__ void add_rows(f32x16& acc, const f32x16& tmp, float s, uint32_t rm, int h) {
+  if (rm == 0xFFFFFFFFu) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[v] += s * tmp[v];
+  } else {
+    const uint32_t mine = rm >> (4 * h);
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const float sum = acc[v] + s * tmp[v];
+      acc[v] = (mine >> (8 * (v >> 2) + (v & 3))) & 1u ? sum : acc[v];
+    }
+  }
+}
+
 // A tile (256 rows x 64 deep, bf16) in LDS: row-major, 8 chunks of 16 bytes
 // per row. The LDS has 64 four-byte banks and serves a 16-byte-per-lane read
 // 16 lanes at a time; a 128-byte row covers half the banks, so rows of one
@@ -104,9 +157,11 @@ struct BScale4 {   // the same for the four steps of a super-step
 // loaded once per super-step. Otherwise they are loaded per step.
 // RSN: chunks of 16 ranks in the LoRA epilogue (1 for r <= 16: t's padding
 // columns 16 .. 31 are zero and skipped; else rank_pad(r) / 16), 0 for none.
-template <bool kQuad, int RSN>
+// kMulti: tab (one weight) has a pool B [n][N][r]; row m uses adapter
+// ml.index[m] of it with ml.scale, and `scale` is not used.
+template <bool kQuad, int RSN, bool kMulti = false>
 __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, int rp, int r, float scale,
-                                                     Codebook cb) {
+                                                     Codebook cb, MultiLora ml) {
   // ring of four x tiles (32 KB each) and the per-wave code slabs (8 KB each),
   // distinct objects so that the compiler can tell a DMA into one from reads
   // of another
@@ -430,7 +485,57 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
           }
       }
     };
-    lora(std::integral_constant<int, RSN>{});
+    // a pool of adapters: for each adapter among the rows, its B fragments
+    // once and the row blocks that hold its rows; t is the row's own already
+    auto lora_multi = [&](auto rsn_c) {
+      constexpr int RS = decltype(rsn_c)::value;
+      constexpr int IG = RS <= 2 ? 8 : RS <= 4 ? 4 : 2;
+      TileAdapters all;
+      all.init(ml, m0, M, lane);
+#pragma unroll
+      for (int i0 = 0; i0 < 8; i0 += IG) {
+        u32x4 tf[IG][RS];
+#pragma unroll
+        for (int ii = 0; ii < IG; ++ii) {
+          const int64_t mrow = imin(m0 + 32 * (i0 + ii) + l32, M - 1);
+#pragma unroll
+          for (int rs = 0; rs < RS; ++rs) tf[ii][rs] = ld16(tl + mrow * rp + 16 * rs + 8 * h);
+        }
+        TileAdapters ta = all;
+        ta.keep(i0, IG);
+        int a;
+        uint64_t rows[4];
+        while (ta.next(a, rows)) {
+          const uint16_t* Ba = Bl + static_cast<int64_t>(a) * N * r;
+          const float s = ml.scale[a];
+          u32x4 bfr[2][RS];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t nrow = imin(n0 + 64 * w + 32 * j + l32, N - 1);
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) bfr[j][rs] = load_row8(Ba + nrow * r, 16 * rs + 8 * h, r, vec_ok);
+          }
+#pragma unroll
+          for (int ii = 0; ii < IG; ++ii) {
+            const uint32_t rm = static_cast<uint32_t>(rows[(i0 + ii) >> 1] >> (32 * ((i0 + ii) & 1)));
+            if (rm == 0) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              f32x16 tmp;
+#pragma unroll
+              for (int v = 0; v < 16; ++v) tmp[v] = 0.f;
+#pragma unroll
+              for (int rs = 0; rs < RS; ++rs) tmp = mfma32(as_bf16x8(tf[ii][rs]), as_bf16x8(bfr[j][rs]), tmp);
+              add_rows(acc[i0 + ii][j], tmp, s, rm, h);
+            }
+          }
+        }
+      }
+    };
+    if constexpr (kMulti)
+      lora_multi(std::integral_constant<int, RSN>{});
+    else
+      lora(std::integral_constant<int, RSN>{});
   }
   // bf16 stores: for fixed (i, j, v) the 32 lanes of a half-wave write 64
   // contiguous bytes of one row; interior tiles skip the bounds checks
@@ -491,14 +596,16 @@ struct BCodes {
 };
 
 // RSN: rank chunks of 16 in the LoRA epilogue (1 for r <= 16, else rank_pad(r) / 16), 0 for none.
-template <int RSN>
+// kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m] with ml.scale.
+template <int RSN, bool kMulti = false>
 __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __restrict__ dy, int64_t M, int64_t N,
                                                             int64_t K, const uint8_t* __restrict__ packed,
                                                             const int8_t* __restrict__ qscale,
                                                             const float* __restrict__ step,
                                                             const uint16_t* __restrict__ ul, int rp,
                                                             const uint16_t* __restrict__ Al, int r, float scale,
-                                                            uint16_t* __restrict__ dx, Codebook cb) {
+                                                            uint16_t* __restrict__ dx, Codebook cb,
+                                                            MultiLora ml) {
   // the two W' buffers are one array: after the main loop it holds A's
   // slice for the LoRA epilogue (up to 128 ranks x 256 columns)
   __shared__ u32x4 As0[kChunks];
@@ -679,8 +786,7 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
     // of 16 that are used (1 for r <= 16: u's padding columns 16 .. 31 are
     // zero and skipped).
     static_assert(16 * 8 * kBwRow <= 2 * kBwChunks, "A's slice does not fit the W' buffers");
-    __syncthreads();
-    {
+    auto stage_a = [&](const uint16_t* Aa) {
       // 16 RSN rows x 32 chunks of 8 columns (K % 64 == 0, so a chunk is
       // wholly inside or past K), all loads before the LDS writes
       constexpr int kPer = 16 * RSN * 32 / kBwThreads;
@@ -689,15 +795,14 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
       for (int u = 0; u < kPer; ++u) {
         const int e = t + kBwThreads * u, j = e >> 5, ch = e & 31;
         const int64_t kc = k0 + 8 * ch;
-        av[u] = (j < r && kc < K) ? ld16(Al + static_cast<int64_t>(j) * K + kc) : u32x4{0u, 0u, 0u, 0u};
+        av[u] = (j < r && kc < K) ? ld16(Aa + static_cast<int64_t>(j) * K + kc) : u32x4{0u, 0u, 0u, 0u};
       }
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int e = t + kBwThreads * u;
         Ws[w_slot(e >> 5, e & 31)] = av[u];
       }
-    }
-    __syncthreads();
+    };
     // groups of IG row blocks: their u fragments are loaded before their
     // MFMAs; A's fragments read per column block
     auto lora = [&](auto rsn_c) {
@@ -730,7 +835,48 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
         }
       }
     };
-    lora(std::integral_constant<int, RSN>{});
+    // a pool of adapters: every adapter among the tile's rows in turn, its
+    // slice of A staged by the whole workgroup, its rows added by their waves
+    auto lora_multi = [&](auto rsn_c) {
+      constexpr int RS = decltype(rsn_c)::value;
+      TileAdapters ta;
+      ta.init(ml, m0, M, lane);
+      int a;
+      uint64_t rows[4];
+      while (ta.next(a, rows)) {
+        __syncthreads();                       // the reads of the slice before (or of the last W' tile)
+        stage_a(Al + static_cast<int64_t>(a) * r * K);
+        __syncthreads();
+        const float s = ml.scale[a];
+        const uint64_t r0 = wm ? rows[2] : rows[0], r1 = wm ? rows[3] : rows[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t rm = static_cast<uint32_t>((i < 2 ? r0 : r1) >> (32 * (i & 1)));
+          if (rm == 0) continue;
+          u32x4 uf[RS];
+          const int64_t mrow = imin(m0 + 128 * wm + 32 * i + l32, M - 1);
+#pragma unroll
+          for (int rs = 0; rs < RS; ++rs) uf[rs] = ld16(ul + mrow * rp + 16 * rs + 8 * h);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f32x16 tmp;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) tmp[v] = 0.f;
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) tmp = mfma32(as_bf16x8(uf[rs]), read_bj(Ws, rs, j), tmp);
+            add_rows(acc[i][j], tmp, s, rm, h);
+          }
+        }
+      }
+    };
+    if constexpr (kMulti) {
+      lora_multi(std::integral_constant<int, RSN>{});
+    } else {
+      __syncthreads();
+      stage_a(Al);
+      __syncthreads();
+      lora(std::integral_constant<int, RSN>{});
+    }
   }
   if (m0 + kTile <= M && k0 + kTile <= K) {
     uint16_t* dt = dx + (m0 + 128 * wm + 4 * h) * K + k0 + 64 * wn + l32;
@@ -802,10 +948,10 @@ static hipError_t launch_fwd_tiled(int64_t M, int G, const uint16_t* const* x, c
   do {                                                                                                         \
     if (quad)                                                                                                  \
       hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fwd<true, RSNV>), dim3(static_cast<unsigned>(tiles)), dim3(256), \
-                         0, stream, tab, M, rp, r, scale, cb);                                                 \
+                         0, stream, tab, M, rp, r, scale, cb, MultiLora{});                                                 \
     else                                                                                                       \
       hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fwd<false, RSNV>), dim3(static_cast<unsigned>(tiles)),          \
-                         dim3(256), 0, stream, tab, M, rp, r, scale, cb);                                      \
+                         dim3(256), 0, stream, tab, M, rp, r, scale, cb, MultiLora{});                                      \
   } while (0)
   mark_kernel(0, stream);
   switch (r == 0 ? 0 : r <= 16 ? 1 : rp / 16) {
@@ -886,7 +1032,8 @@ hipError_t launch_bwd_dx(const uint16_t* dy, int64_t M, int64_t N, int64_t K, co
 #define QNF4_BWD(RSNV)                                                                                         \
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_bwd<RSNV>), dim3(static_cast<unsigned>(tiles)), dim3(kBwThreads), 0, \
                      stream,                                                                                  \
-                     dy, M, N, K, packed, qscale, step, static_cast<const uint16_t*>(lora), rp, A, r, scale, dx, cb)
+                     dy, M, N, K, packed, qscale, step, static_cast<const uint16_t*>(lora), rp, A, r, scale, dx, cb, \
+                     MultiLora{})
   mark_kernel(0, stream);
   switch (r == 0 ? 0 : r <= 16 ? 1 : rp / 16) {
     case 0: QNF4_BWD(0); break;
@@ -897,6 +1044,83 @@ hipError_t launch_bwd_dx(const uint16_t* dy, int64_t M, int64_t N, int64_t K, co
     default: QNF4_BWD(8); break;
   }
 #undef QNF4_BWD
+  mark_kernel(1, stream);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// a pool of adapters: t or u of every row (launch_multi_down), then the tiled
+// GEMM with the row-by-row epilogue
+// ---------------------------------------------------------------------------
+size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
+  if (op == 2) return multi_grad_plan(M, N, K, r, n, true).total;
+  return kWsCounterBytes + align256(static_cast<size_t>(M * rank_pad(r) * 2));
+}
+
+hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                            const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                            const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,
+                            hipStream_t stream) {
+  uint16_t* tl = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
+  const hipError_t e = launch_multi_down(true, x, M, K, A, ml.n, ml.index, r, tl, stream);
+  if (e != hipSuccess) return e;
+  const int rp = static_cast<int>(rank_pad(r));
+  FwdTable tab{};
+  tab.count = 1;
+  tab.x[0] = x;
+  tab.packed[0] = packed;
+  tab.qscale[0] = qscale;
+  tab.step[0] = step;
+  tab.tl[0] = tl;
+  tab.B[0] = B;
+  tab.y[0] = y;
+  tab.N[0] = static_cast<int>(N);
+  tab.K[0] = static_cast<int>(K);
+  tab.col0[1] = static_cast<int>(cdiv(N, kTile));
+  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(N, kTile)));
+#define QNF4_MFWD(RSNV)                                                                                        \
+  do {                                                                                                         \
+    if (K % 256 == 0)                                                                                          \
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fwd<true, RSNV, true>), grid, dim3(256), 0, stream, tab, M, rp, r, \
+                         0.0f, cb, ml);                                                                        \
+    else                                                                                                       \
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_fwd<false, RSNV, true>), grid, dim3(256), 0, stream, tab, M, rp, r, \
+                         0.0f, cb, ml);                                                                        \
+  } while (0)
+  mark_kernel(0, stream);
+  switch (r <= 16 ? 1 : rp / 16) {
+    case 1: QNF4_MFWD(1); break;
+    case 2: QNF4_MFWD(2); break;
+    case 4: QNF4_MFWD(4); break;
+    case 6: QNF4_MFWD(6); break;
+    default: QNF4_MFWD(8); break;
+  }
+#undef QNF4_MFWD
+  mark_kernel(1, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                            const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                            const MultiLora& ml, int r, uint16_t* dx, void* ws, const Codebook& cb,
+                            hipStream_t stream) {
+  uint16_t* ul = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
+  const hipError_t e = launch_multi_down(false, dy, M, N, B, ml.n, ml.index, r, ul, stream);
+  if (e != hipSuccess) return e;
+  const int rp = static_cast<int>(rank_pad(r));
+  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(K, kTile)));
+#define QNF4_MBWD(RSNV)                                                                                       \
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_bwd<RSNV, true>), grid, dim3(kBwThreads), 0, stream, dy, M, N, K, packed, \
+                     qscale, step, static_cast<const uint16_t*>(ul), rp, A, r, 0.0f, dx, cb, ml)
+  mark_kernel(0, stream);
+  switch (r <= 16 ? 1 : rp / 16) {
+    case 1: QNF4_MBWD(1); break;
+    case 2: QNF4_MBWD(2); break;
+    case 4: QNF4_MBWD(4); break;
+    case 6: QNF4_MBWD(6); break;
+    default: QNF4_MBWD(8); break;
+  }
+#undef QNF4_MBWD
   mark_kernel(1, stream);
   return hipGetLastError();
 }

@@ -238,6 +238,69 @@ hipError_t launch_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M, in
                             const uint16_t* A, const uint16_t* B, int r, float alpha, float* dA, float* dB,
                             int accumulate, void* ws, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// A pool of adapters beside one weight (multi.hip; the GEMMs in gemm.hip):
+// row m of the batch uses adapter index[m] of A [n][r][K], B [n][N][r], scale
+// [n]; an index outside 0 .. n - 1 means none.
+// ---------------------------------------------------------------------------
+constexpr int kMaxAdapters = 4096;
+struct MultiLora {
+  const int* index;         // [M]
+  const float* scale;       // [n]
+  int n;
+};
+
+// t = bf16(x . A_a^T) (wrow: in = x, Kc = K, W = A) or u = bf16(dY . B_a) (in =
+// dY, Kc = N, W = B) of every row with an adapter: bf16 [M][rank_pad(r)]
+hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t Kc, const uint16_t* W, int n,
+                             const int* index, int r, uint16_t* out, hipStream_t stream);
+hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                            const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                            const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,
+                            hipStream_t stream);
+hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                            const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                            const MultiLora& ml, int r, uint16_t* dx, void* ws, const Codebook& cb,
+                            hipStream_t stream);
+size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n);
+
+// Gradients: the rows of each adapter listed in chunks of 64 places (a place
+// without a row holds -1), the chunks of an adapter cut into items.
+struct GradItem {
+  int adapter, c0, c1;      // chunks [c0, c1)
+  int slot;                 // partial sums, or -1: the adapter's only item, written in place
+};
+struct GradAdapter {
+  int items, slot;          // items of the adapter, its first partial slot (items > 1)
+};
+struct GradLists {
+  int* rows;                // [chunks * 64]; null: one adapter, every row in order
+  int* chunk_adapter;       // [chunks]
+  GradItem* item;
+  GradAdapter* adapter;     // [n]
+  int* total;               // chunks, items
+};
+struct MultiGradPlan {
+  int nt = 1;               // rank tiles of 16 (a power of two)
+  int64_t chunks = 0, Mp = 0, per_item = 1, items = 0, slots = 0;   // chunks, items and slots at most
+  size_t rows_off = 0, chunk_off = 0, item_off = 0, adapter_off = 0, total_off = 0;
+  size_t tt_off = 0, ut_off = 0, pa_off = 0, pb_off = 0, total = 0;
+};
+MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, bool listed);
+// xfmt: kActBf16 (x bf16), or the format of a checkpoint (x its codes, tops its
+// block constants). index == null: one adapter (n = 1) for every row; scale ==
+// null: alpha_r.
+hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, const uint16_t* dy, int64_t M, int64_t N,
+                             int64_t K, const uint16_t* A, const uint16_t* B, const float* scale, float alpha_r, int n,
+                             const int* index, int r, float* dA, float* dB, int accumulate, void* ws,
+                             hipStream_t stream);
+
+// 8-bit activation checkpoints (act8.hip); numel a multiple of 64
+hipError_t launch_act8_pack(const uint16_t* x, int64_t numel, int fmt, uint8_t* codes, uint16_t* absmax,
+                            hipStream_t stream);
+hipError_t launch_act8_unpack(const uint8_t* codes, const uint16_t* absmax, int64_t numel, int fmt, uint16_t* out,
+                              hipStream_t stream);
+
 // Measurement events (set through the C ABI): when set, mark_kernel(0, s)
 // records the start event and mark_kernel(1, s) the stop event on stream s,
 // right around the main kernel of a matmul call.

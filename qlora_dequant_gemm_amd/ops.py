@@ -5,6 +5,7 @@ all in the library's kernels. bf16 tensors are passed as their 16-bit
 patterns, which is what the ABI expects.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -397,7 +398,11 @@ def bwd_dx_batched(dys, qws, As=None, Bs=None, alpha=0.0, outs=None, ws=None):
 def lora_grad(x, dy, A, B, alpha, dA=None, dB=None, accumulate=False, ws=None):
     """Adapter gradients (dA [r, K], dB [N, r], fp32) of one QLoRA linear:
     dB = (alpha/r) . dY^T . bf16(x . A^T), dA = (alpha/r) . bf16(dY . B)^T . x.
-    With accumulate=True they are added to dA and dB."""
+    With accumulate=True they are added to dA and dB. x may be the layer input
+    kept in 8 bits (an Act8): the gradients are then those of its restored
+    values, read from the codes directly, with x . A^T and dY . B not rounded."""
+    if isinstance(x, Act8):
+        return _lora_grad_act8(x, dy, A, B, alpha, dA, dB, accumulate, ws)
     M = _rows(x, "x")
     _rows(dy, "dy")
     K, N = x.shape[1], dy.shape[1]
@@ -422,6 +427,239 @@ def lora_grad(x, dy, A, B, alpha, dA=None, dB=None, accumulate=False, ws=None):
     _lib.check("qlora_lora_grad", _lib.lib().qlora_lora_grad(
         _ptr(x), _ptr(dy), M, N, K, _ptr(A), _ptr(B), r, float(alpha), _ptr(dA), _ptr(dB),
         1 if accumulate else 0, _ptr(wsb), 0 if wsb is None else wsb.numel(), _stream(x.device)))
+    return dA, dB
+
+
+# ---------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+_ACT = {"int8": (0, torch.int8), "e4m3": (1, torch.uint8)}
+_ACT_BF16 = 2
+
+
+def _act_fmt(fmt):
+    if fmt not in _ACT:
+        raise ValueError(f"fmt must be one of {sorted(_ACT)}, got {fmt!r}")
+    return _ACT[fmt]
+
+
+def _launch(fn, dev, *args):
+    """Calls entry point `fn` on `dev`'s current stream, with `dev` current."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(_lib.lib(), fn)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib.lib(), fn)(*args, stream)
+    if status:
+        _lib.check(fn, status)
+
+
+class Act8:
+    """An activation kept in 8 bits: codes of its shape [..., K] (int8 for
+    "int8", the e4m3 bits as uint8 for "e4m3") and one bf16 constant per 64
+    values, absmax [numel / 64]."""
+
+    def __init__(self, codes, absmax, fmt="int8"):
+        _, dt = _act_fmt(fmt)
+        if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or codes.numel() == 0 or codes.shape[-1] % BLOCK:
+            raise ValueError(f"codes must be a non-empty tensor whose last dimension is a multiple of {BLOCK}")
+        _shape(absmax, (codes.numel() // BLOCK,), "absmax")
+        _need(codes, dt, "codes")
+        _need(absmax, torch.bfloat16, "absmax", codes.device)
+        self.codes, self.absmax, self.fmt, self.shape = codes, absmax, fmt, tuple(codes.shape)
+
+    @property
+    def nbytes(self):
+        return self.codes.nbytes + self.absmax.nbytes
+
+
+def act8_pack(x, fmt="int8"):
+    """bf16 x [..., K] (K a multiple of 64) -> Act8: per block of 64, top = max
+    |x| and code = rne(127 x / top) ("int8") or the e4m3 value nearest 448 x /
+    top ("e4m3"). A block with a NaN or an infinity restores to NaN, one below
+    2^-80 to zeros."""
+    code, dt = _act_fmt(fmt)
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.numel() == 0 or x.shape[-1] % BLOCK:
+        raise ValueError(f"x must be a non-empty tensor whose last dimension is a multiple of {BLOCK}")
+    _need(x, torch.bfloat16, "x")
+    kept = Act8.__new__(Act8)
+    kept.codes = torch.empty(x.shape, dtype=dt, device=x.device)
+    kept.absmax = torch.empty(x.numel() // BLOCK, dtype=torch.bfloat16, device=x.device)
+    kept.fmt, kept.shape = fmt, tuple(x.shape)
+    _launch("qlora_act8_pack", x.device, x.data_ptr(), x.numel(), code, kept.codes.data_ptr(), kept.absmax.data_ptr())
+    return kept
+
+
+def act8_unpack(kept, out=None):
+    """The bf16 activation that an Act8 stands for: bf16(code * fp32(top / 127))
+    or bf16(code * fp32(top / 448))."""
+    dev = kept.codes.device
+    if out is not None:
+        _shape(out, kept.shape, "out")
+    out = _check_out(out, kept.shape, dev, "out")
+    _launch("qlora_act8_unpack", dev, kept.codes.data_ptr(), kept.absmax.data_ptr(), kept.codes.numel(),
+            _ACT[kept.fmt][0], out.data_ptr())
+    return out
+
+
+def _act8_rows(kept, name):
+    if len(kept.shape) != 2:
+        raise ValueError(f"{name} must be two-dimensional, got {kept.shape}")
+    return kept.shape
+
+
+def _lora_grad_act8(x, dy, A, B, alpha, dA, dB, accumulate, ws):
+    M, K = _act8_rows(x, "x")
+    N = dy.shape[1] if _rows(dy, "dy") == M else 0
+    _shape(dy, (M, N), "dy")
+    r = _adapter_rank(A, B, N, K)
+    if r == 0:
+        raise ValueError("adapter gradients need adapters")
+    if dA is not None:
+        _shape(dA, (r, K), "dA")
+    if dB is not None:
+        _shape(dB, (N, r), "dB")
+    dev = x.codes.device
+    _need(dy, torch.bfloat16, "dy", dev)
+    _check_adapters(A, B, N, K, dev)
+    dA = _grad_out(dA, (r, K), accumulate, dev, "dA")
+    dB = _grad_out(dB, (N, r), accumulate, dev, "dB")
+    wsb = _workspace(ws, dev, 3, M, N, K, r, 1)
+    _launch("qlora_lora_grad_act8", dev, x.codes.data_ptr(), x.absmax.data_ptr(), _ACT[x.fmt][0], dy.data_ptr(),
+            M, N, K, A.data_ptr(), B.data_ptr(), r, float(alpha), dA.data_ptr(), dB.data_ptr(), int(bool(accumulate)),
+            wsb.data_ptr(), wsb.numel())
+    return dA, dB
+
+
+# ---------------------------------------------------------------------------
+# a pool of adapters beside one weight
+# ---------------------------------------------------------------------------
+MAX_ADAPTERS = 4096
+
+
+class AdapterPool:
+    """Adapters that share one frozen weight [N, K]: A [n, r, K] and B [n, N, r]
+    bf16, scale [n] fp32 (alpha / r of each). Adapters of a smaller rank are
+    padded with zeros."""
+
+    def __init__(self, A, B, scale):
+        for t, name in ((A, "A"), (B, "B")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3:
+                raise ValueError(f"{name} must be a three-dimensional tensor")
+        n, r, K = A.shape
+        N = B.shape[1]
+        _shape(B, (n, N, r), "B")
+        _shape(scale, (n,), "scale")
+        if not 1 <= n <= MAX_ADAPTERS or not 1 <= r <= 128:
+            raise ValueError(f"a pool holds 1 to {MAX_ADAPTERS} adapters of rank 1 to 128, got {n} of rank {r}")
+        _need(A, torch.bfloat16, "A")
+        _need(B, torch.bfloat16, "B", A.device)
+        _need(scale, torch.float32, "scale", A.device)
+        self.A, self.B, self.scale = A, B, scale
+        self.n, self.r, self.N, self.K = n, r, N, K
+
+
+@functools.lru_cache(maxsize=4096)
+def workspace_bytes_multi(op, M, N, K, r, n):
+    return int(_lib.lib().qlora_workspace_bytes_multi(op, M, N, K, r, n))
+
+
+def _workspace(ws, dev, op, M, N, K, r, n):
+    need = workspace_bytes_multi(op, M, N, K, r, n)
+    if need == 0:
+        raise ValueError(f"sizes out of range: M {M}, N {N}, K {K}, rank {r}, {n} adapters")
+    buf = (ws or Workspace(dev)).get(need)
+    if buf.device != dev:
+        raise ValueError(f"the workspace is on {buf.device}, expected {dev}")
+    return buf
+
+
+def _grad_out(t, shape, accumulate, dev, name):
+    if t is None:
+        return (torch.zeros if accumulate else torch.empty)(shape, dtype=torch.float32, device=dev)
+    _need(t, torch.float32, name, dev, shape=shape)
+    return t
+
+
+def _check_pool(pool, index, M, N, K, dev):
+    if (pool.N, pool.K) != (N, K):
+        raise ValueError(f"the pool's adapters are for [{pool.N}, {pool.K}], expected [{N}, {K}]")
+    _shape(index, (M,), "index")
+    if pool.A.device != dev:
+        raise ValueError(f"the pool is on {pool.A.device}, expected {dev}")
+    _need(index, torch.int32, "index", dev)
+
+
+def lora_fwd_multi(x, qw, pool, index, out=None, ws=None):
+    """The forward of a batch whose rows use different adapters of a pool:
+    y_m = x_m . deq(W)^T + s_a . (x_m . A_a^T) . B_a^T with a = index[m] (int32
+    [M] on the device); a row whose index is outside 0 .. n - 1 takes the base
+    alone. bf16 [M, K] -> [M, N]."""
+    N, K = qw.shape
+    M = _rows(x, "x")
+    _shape(x, (M, K), "x")
+    if out is not None:
+        _shape(out, (M, N), "out")
+    dev = x.device
+    _check_pool(pool, index, M, N, K, dev)
+    _need(x, torch.bfloat16, "x")
+    _check_weight(qw, dev)
+    out = _check_out(out, (M, N), dev, "out")
+    wsb = _workspace(ws, dev, 0, M, N, K, pool.r, pool.n)
+    _launch("qlora_nf4_lora_fwd_multi", dev, x.data_ptr(), M, N, K, qw.packed.data_ptr(), qw.qscale.data_ptr(),
+            qw.step.data_ptr(), pool.A.data_ptr(), pool.B.data_ptr(), pool.scale.data_ptr(), pool.n,
+            index.data_ptr(), pool.r, out.data_ptr(), wsb.data_ptr(), wsb.numel())
+    return out
+
+
+def bwd_dx_multi(dy, qw, pool, index, out=None, ws=None):
+    """The backward to the input of lora_fwd_multi: dX_m = dY_m . deq(W) +
+    s_a . (dY_m . B_a) . A_a, a = index[m]. bf16 [M, N] -> [M, K]."""
+    N, K = qw.shape
+    M = _rows(dy, "dy")
+    _shape(dy, (M, N), "dy")
+    if out is not None:
+        _shape(out, (M, K), "out")
+    dev = dy.device
+    _check_pool(pool, index, M, N, K, dev)
+    _need(dy, torch.bfloat16, "dy")
+    _check_weight(qw, dev)
+    out = _check_out(out, (M, K), dev, "out")
+    wsb = _workspace(ws, dev, 1, M, N, K, pool.r, pool.n)
+    _launch("qlora_nf4_bwd_dx_multi", dev, dy.data_ptr(), M, N, K, qw.packed.data_ptr(), qw.qscale.data_ptr(),
+            qw.step.data_ptr(), pool.A.data_ptr(), pool.B.data_ptr(), pool.scale.data_ptr(), pool.n,
+            index.data_ptr(), pool.r, out.data_ptr(), wsb.data_ptr(), wsb.numel())
+    return out
+
+
+def lora_grad_multi(x, dy, pool, index, dA=None, dB=None, accumulate=False, ws=None):
+    """Gradients of every adapter of a pool (dA [n, r, K], dB [n, N, r], fp32)
+    from a batch whose row m uses adapter index[m]: dB_a = s_a sum_m dY_m^T
+    (x_m . A_a^T), dA_a = s_a sum_m (dY_m . B_a)^T x_m over the rows of a;
+    zeros for an adapter without rows. x is bf16 [M, K] or an Act8 of it. With
+    accumulate=True they are added to dA and dB."""
+    kept = isinstance(x, Act8)
+    M, K = _act8_rows(x, "x") if kept else (_rows(x, "x"), x.shape[1])
+    xt = x.codes if kept else x
+    dev = xt.device
+    _shape(dy, (M, pool.N), "dy")
+    N, r, n = pool.N, pool.r, pool.n
+    if dA is not None:
+        _shape(dA, (n, r, K), "dA")
+    if dB is not None:
+        _shape(dB, (n, N, r), "dB")
+    _check_pool(pool, index, M, N, K, dev)
+    if not kept:
+        _need(x, torch.bfloat16, "x")
+    _need(dy, torch.bfloat16, "dy", dev)
+    dA = _grad_out(dA, (n, r, K), accumulate, dev, "dA")
+    dB = _grad_out(dB, (n, N, r), accumulate, dev, "dB")
+    wsb = _workspace(ws, dev, 2, M, N, K, r, n)
+    _launch("qlora_lora_grad_multi", dev, xt.data_ptr(), _ACT[x.fmt][0] if kept else _ACT_BF16,
+            x.absmax.data_ptr() if kept else 0, dy.data_ptr(), M, N, K, pool.A.data_ptr(), pool.B.data_ptr(),
+            pool.scale.data_ptr(), n, index.data_ptr(), r, dA.data_ptr(), dB.data_ptr(), int(bool(accumulate)),
+            wsb.data_ptr(), wsb.numel())
     return dA, dB
 
 

@@ -371,10 +371,10 @@ int qlora_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M,
  * (or the gradients) that use it. Every pointer is 16-byte aligned except scale
  * and index (4 bytes). M < 2^31; sizes otherwise as in qlora_nf4_lora_fwd.
  *
- * qlora_nf4_lora_fwd_multi:  y_m  = bf16( x_m . W'^T + s_a . t_m . B_a^T ),
- *                            t_m  = bf16(x_m . A_a^T),  a = index[m]
- * qlora_nf4_bwd_dx_multi:    dX_m = bf16( dY_m . W' + s_a . u_m . A_a ),
- *                            u_m  = bf16(dY_m . B_a);  N a multiple of 8
+ * qlora_nf4_lora_fwd_multi:  y_m  = bf16( x_m . W'^T + t_m . B_a^T ),
+ *                            t_m  = bf16(s_a . x_m . A_a^T),  a = index[m]
+ * qlora_nf4_bwd_dx_multi:    dX_m = bf16( dY_m . W' + u_m . A_a ),
+ *                            u_m  = bf16(s_a . dY_m . B_a);  N a multiple of 8
  * qlora_lora_grad_multi:     dB_a = s_a sum_m dY_m^T (x_m . A_a^T)   [n, N, r]
  *                            dA_a = s_a sum_m (dY_m . B_a)^T x_m     [n, r, K]
  *     over the rows m of adapter a, fp32; t and u enter as three bf16 numbers

@@ -18,7 +18,7 @@ OBJ = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["codebook.cpp", "api.cpp", "quant.hip", "lora.hip", "small.hip", "decode.hip", "gemm.hip", "grad.hip", "merge.hip",
-           "noalloc.hip", "multi.hip", "act8.hip"]
+           "noalloc.hip", "multi.hip", "mstream.hip", "act8.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

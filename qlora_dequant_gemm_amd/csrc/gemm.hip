@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "mm_common.hpp"
+#include "multi.hpp"
 
 namespace qnf4 {
 
@@ -50,57 +51,26 @@ __device__ __forceinline__ void tile_of(int pid, int ntm, int ntn, int& tm, int&
   tn = within / gsz;
 }
 
-// The adapters among the 256 rows of a tile, one after another in the order
-// of their first rows: next() gives an adapter and the rows that use it (row
-// 64 q + b is bit b of rows[q]), wave-uniform and the same in every wave.
-struct TileAdapters {
+// The adapters of the 256 rows of a tile: lane l has those of rows 64 q + l.
+struct TileRows {
   int id[4];
-  uint64_t pend[4];
   __device__ __forceinline__ void init(const MultiLora& ml, int64_t m0, int64_t M, int lane) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t m = m0 + 64 * q + lane;
       id[q] = m < M ? ml.index[m] : -1;
       if (static_cast<unsigned>(id[q]) >= static_cast<unsigned>(ml.n)) id[q] = -1;
-      pend[q] = __ballot(id[q] >= 0);
     }
-  }
-  // leave out the rows outside [32 i0, 32 (i0 + count))
-  __device__ __forceinline__ void keep(int i0, int count) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < i0 || i >= i0 + count) pend[i >> 1] &= ~(0xFFFFFFFFull << (32 * (i & 1)));
-  }
-  __device__ __forceinline__ bool next(int& a, uint64_t (&rows)[4]) {
-    if (!(pend[0] | pend[1] | pend[2] | pend[3])) return false;
-    a = pend[0]   ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pend[0]))
-        : pend[1] ? __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pend[1]))
-        : pend[2] ? __builtin_amdgcn_readlane(id[2], __builtin_ctzll(pend[2]))
-                  : __builtin_amdgcn_readlane(id[3], __builtin_ctzll(pend[3]));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      rows[q] = __ballot(id[q] == a);
-      pend[q] &= ~rows[q];
-    }
-    return true;
   }
 };
 
-// acc += s * tmp on the rows of a 32 x 32 block that `rm` names (bit = row).
-// A row that is not named keeps its bits whatever tmp holds there: a NaN in
-// one adapter must not reach the rows of another.
-__device__ __forceinline__ void add_rows(f32x16& acc, const f32x16& tmp, float s, uint32_t rm, int h) {
-  if (rm == 0xFFFFFFFFu) {
+// rows of a 32 x 32 block that `rm` names (bit = row) from p, the others as
+// they are: a NaN in one adapter must not reach the rows of another, so the
+// choice is made after the product
+__device__ __forceinline__ void take_rows(f32x16& tmp, const f32x16& p, uint32_t rm, int h) {
+  const uint32_t mine = rm >> (4 * h);
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] += s * tmp[v];
-  } else {
-    const uint32_t mine = rm >> (4 * h);
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const float sum = acc[v] + s * tmp[v];
-      acc[v] = (mine >> (8 * (v >> 2) + (v & 3))) & 1u ? sum : acc[v];
-    }
-  }
+  for (int v = 0; v < 16; ++v) tmp[v] = (mine >> (8 * (v >> 2) + (v & 3))) & 1u ? p[v] : tmp[v];
 }
 
 // A tile (256 rows x 64 deep, bf16) in LDS: row-major, 8 chunks of 16 bytes
@@ -158,7 +128,7 @@ struct BScale4 {   // the same for the four steps of a super-step
 // RSN: chunks of 16 ranks in the LoRA epilogue (1 for r <= 16: t's padding
 // columns 16 .. 31 are zero and skipped; else rank_pad(r) / 16), 0 for none.
 // kMulti: tab (one weight) has a pool B [n][N][r]; row m uses adapter
-// ml.index[m] of it with ml.scale, and `scale` is not used.
+// ml.index[m] of it; t carries the scale (`scale` is not used).
 template <bool kQuad, int RSN, bool kMulti = false>
 __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, int rp, int r, float scale,
                                                      Codebook cb, MultiLora ml) {
@@ -485,13 +455,18 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
           }
       }
     };
-    // a pool of adapters: for each adapter among the rows, its B fragments
-    // once and the row blocks that hold its rows; t is the row's own already
+    // a pool of adapters: block by block of 32 rows, the adapters among them
+    // (mostly one: rows of a request follow each other); an adapter's B
+    // fragments are kept until another one is needed. The sums of a block are
+    // added once, outside the loop over its adapters, so that the
+    // accumulators stay where they are. t carries the scale.
     auto lora_multi = [&](auto rsn_c) {
       constexpr int RS = decltype(rsn_c)::value;
       constexpr int IG = RS <= 2 ? 8 : RS <= 4 ? 4 : 2;
-      TileAdapters all;
-      all.init(ml, m0, M, lane);
+      TileRows tr;
+      tr.init(ml, m0, M, lane);
+      u32x4 bfr[2][RS];
+      int have = -1;
 #pragma unroll
       for (int i0 = 0; i0 < 8; i0 += IG) {
         u32x4 tf[IG][RS];
@@ -501,34 +476,44 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
 #pragma unroll
           for (int rs = 0; rs < RS; ++rs) tf[ii][rs] = ld16(tl + mrow * rp + 16 * rs + 8 * h);
         }
-        TileAdapters ta = all;
-        ta.keep(i0, IG);
-        int a;
-        uint64_t rows[4];
-        while (ta.next(a, rows)) {
-          const uint16_t* Ba = Bl + static_cast<int64_t>(a) * N * r;
-          const float s = ml.scale[a];
-          u32x4 bfr[2][RS];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t nrow = imin(n0 + 64 * w + 32 * j + l32, N - 1);
+        for (int ii = 0; ii < IG; ++ii) {
+          const int i = i0 + ii;
+          const int id = tr.id[i >> 1];
+          uint64_t pend = __ballot(id >= 0) & (0xFFFFFFFFull << (32 * (i & 1)));
+          f32x16 tmp[2];
 #pragma unroll
-            for (int rs = 0; rs < RS; ++rs) bfr[j][rs] = load_row8(Ba + nrow * r, 16 * rs + 8 * h, r, vec_ok);
-          }
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int ii = 0; ii < IG; ++ii) {
-            const uint32_t rm = static_cast<uint32_t>(rows[(i0 + ii) >> 1] >> (32 * ((i0 + ii) & 1)));
-            if (rm == 0) continue;
+            for (int v = 0; v < 16; ++v) tmp[j][v] = 0.f;
+          while (pend) {
+            const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(pend));
+            const uint64_t rows = __ballot(id == a) & pend;
+            pend &= ~rows;
+            if (a != have) {
+              have = a;
+              const uint16_t* Ba = Bl + static_cast<int64_t>(a) * N * r;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int64_t nrow = imin(n0 + 64 * w + 32 * j + l32, N - 1);
+#pragma unroll
+                for (int rs = 0; rs < RS; ++rs) bfr[j][rs] = load_row8(Ba + nrow * r, 16 * rs + 8 * h, r, vec_ok);
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              f32x16 tmp;
+              f32x16 p;
 #pragma unroll
-              for (int v = 0; v < 16; ++v) tmp[v] = 0.f;
+              for (int v = 0; v < 16; ++v) p[v] = 0.f;
 #pragma unroll
-              for (int rs = 0; rs < RS; ++rs) tmp = mfma32(as_bf16x8(tf[ii][rs]), as_bf16x8(bfr[j][rs]), tmp);
-              add_rows(acc[i0 + ii][j], tmp, s, rm, h);
+              for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(tf[ii][rs]), as_bf16x8(bfr[j][rs]), p);
+              take_rows(tmp[j], p, static_cast<uint32_t>(rows >> (32 * (i & 1))), h);
             }
           }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] += tmp[j][v];
         }
       }
     };
@@ -596,7 +581,7 @@ struct BCodes {
 };
 
 // RSN: rank chunks of 16 in the LoRA epilogue (1 for r <= 16, else rank_pad(r) / 16), 0 for none.
-// kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m] with ml.scale.
+// kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m]; u carries the scale.
 template <int RSN, bool kMulti = false>
 __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __restrict__ dy, int64_t M, int64_t N,
                                                             int64_t K, const uint8_t* __restrict__ packed,
@@ -835,37 +820,51 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
         }
       }
     };
-    // a pool of adapters: every adapter among the tile's rows in turn, its
-    // slice of A staged by the whole workgroup, its rows added by their waves
+    // a pool of adapters: every adapter among the tile's rows in turn (the
+    // same order in every wave), its slice of A staged by the whole workgroup;
+    // straight-line code over the wave's blocks, so that the accumulators
+    // stay where they are. u carries the scale.
     auto lora_multi = [&](auto rsn_c) {
       constexpr int RS = decltype(rsn_c)::value;
-      TileAdapters ta;
-      ta.init(ml, m0, M, lane);
-      int a;
-      uint64_t rows[4];
-      while (ta.next(a, rows)) {
+      TileRows tr;
+      tr.init(ml, m0, M, lane);
+      uint64_t pend[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) pend[q] = __ballot(tr.id[q] >= 0);
+      while (pend[0] | pend[1] | pend[2] | pend[3]) {
+        const int a = pend[0]   ? __builtin_amdgcn_readlane(tr.id[0], __builtin_ctzll(pend[0]))
+                      : pend[1] ? __builtin_amdgcn_readlane(tr.id[1], __builtin_ctzll(pend[1]))
+                      : pend[2] ? __builtin_amdgcn_readlane(tr.id[2], __builtin_ctzll(pend[2]))
+                                : __builtin_amdgcn_readlane(tr.id[3], __builtin_ctzll(pend[3]));
+        uint64_t rows[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          rows[q] = __ballot(tr.id[q] == a);
+          pend[q] &= ~rows[q];
+        }
         __syncthreads();                       // the reads of the slice before (or of the last W' tile)
         stage_a(Al + static_cast<int64_t>(a) * r * K);
         __syncthreads();
-        const float s = ml.scale[a];
         const uint64_t r0 = wm ? rows[2] : rows[0], r1 = wm ? rows[3] : rows[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t rm = static_cast<uint32_t>((i < 2 ? r0 : r1) >> (32 * (i & 1)));
-          if (rm == 0) continue;
           u32x4 uf[RS];
           const int64_t mrow = imin(m0 + 128 * wm + 32 * i + l32, M - 1);
 #pragma unroll
           for (int rs = 0; rs < RS; ++rs) uf[rs] = ld16(ul + mrow * rp + 16 * rs + 8 * h);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            f32x16 tmp;
+            f32x16 p, tmp;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) tmp[v] = 0.f;
+            for (int v = 0; v < 16; ++v) p[v] = tmp[v] = 0.f;
 #pragma unroll
-            for (int rs = 0; rs < RS; ++rs) tmp = mfma32(as_bf16x8(uf[rs]), read_bj(Ws, rs, j), tmp);
-            add_rows(acc[i][j], tmp, s, rm, h);
+            for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(uf[rs]), read_bj(Ws, rs, j), p);
+            take_rows(tmp, p, rm, h);
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] += tmp[v];
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     };
@@ -1054,6 +1053,7 @@ hipError_t launch_bwd_dx(const uint16_t* dy, int64_t M, int64_t N, int64_t K, co
 // ---------------------------------------------------------------------------
 size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
   if (op == 2) return multi_grad_plan(M, N, K, r, n, true).total;
+  if (op == 0 && M <= kMsMaxM) return ms_plan(M, N, K, r).total;
   return kWsCounterBytes + align256(static_cast<size_t>(M * rank_pad(r) * 2));
 }
 
@@ -1061,8 +1061,10 @@ hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, 
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
                             const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,
                             hipStream_t stream) {
+  if (M <= kMsMaxM)
+    return launch_mstream(ms_plan(M, N, K, r), x, M, N, K, packed, qscale, step, A, B, ml, r, y, ws, cb, stream);
   uint16_t* tl = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
-  const hipError_t e = launch_multi_down(true, x, M, K, A, ml.n, ml.index, r, tl, stream);
+  const hipError_t e = launch_multi_down(true, x, M, K, A, ml, r, tl, stream);
   if (e != hipSuccess) return e;
   const int rp = static_cast<int>(rank_pad(r));
   FwdTable tab{};
@@ -1105,7 +1107,7 @@ hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K,
                             const MultiLora& ml, int r, uint16_t* dx, void* ws, const Codebook& cb,
                             hipStream_t stream) {
   uint16_t* ul = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
-  const hipError_t e = launch_multi_down(false, dy, M, N, B, ml.n, ml.index, r, ul, stream);
+  const hipError_t e = launch_multi_down(false, dy, M, N, B, ml, r, ul, stream);
   if (e != hipSuccess) return e;
   const int rp = static_cast<int>(rank_pad(r));
   const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(K, kTile)));

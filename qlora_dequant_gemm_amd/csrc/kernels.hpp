@@ -250,10 +250,6 @@ struct MultiLora {
   int n;
 };
 
-// t = bf16(x . A_a^T) (wrow: in = x, Kc = K, W = A) or u = bf16(dY . B_a) (in =
-// dY, Kc = N, W = B) of every row with an adapter: bf16 [M][rank_pad(r)]
-hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t Kc, const uint16_t* W, int n,
-                             const int* index, int r, uint16_t* out, hipStream_t stream);
 hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
                             const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,

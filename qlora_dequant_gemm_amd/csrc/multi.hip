@@ -9,8 +9,9 @@
 //     t_m = x_m . A_a^T,  u_m = dY_m . B_a
 //     dB_a = s_a sum_m dY_m^T t_m,   dA_a = s_a sum_m u_m^T x_m   (rows m of a)
 //
-// k_mdown  t or u of a batch in its own order, for the forward and backward
-//          GEMMs: 16 rows per workgroup, one pass per adapter among them.
+// k_mdown  s_a t or s_a u of a batch in its own order, for the forward and
+//          backward GEMMs: 16 rows per workgroup, one pass per adapter among
+//          them; beside it, x in MFMA order for the streaming forward.
 // The gradients first list each adapter's rows (k_msort: the rows of an adapter in
 // batch order, padded to whole 64-row chunks), so that every later product has
 // one adapter per chunk and needs no masks:
@@ -31,6 +32,7 @@
 
 #include "act8.hpp"
 #include "mm_common.hpp"
+#include "multi.hpp"
 
 namespace qnf4 {
 
@@ -100,12 +102,8 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, i
           const int pc = lane + 64 * e, Rw = (pc >> 1) / RT, col = 16 * ((pc >> 1) % RT) + 8 * (pc & 1);
           const int n = q * 64 + Rw;
           const uint16_t* wr = W + static_cast<int64_t>(n < Kc ? n : 0) * r;
-          if (vec) {
-            const u32x4 v = ld16(wr + (col < r ? col : 0));
-            R.wv[u][e] = col < r && n < Kc ? v : zero;
-          } else {
-            R.wv[u][e] = n < Kc ? load_row8(wr, col, r, false) : zero;
-          }
+          if (vec) R.wv[u][e] = ld16(wr + (col < r ? col : 0));   // cleared when it is staged
+          else R.wv[u][e] = load_row8(wr, col, r, false);
         }
       } else {
 #pragma unroll
@@ -124,8 +122,10 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, i
       for (int u = 0; u < GS; ++u)
 #pragma unroll
         for (int e = 0; e < 2 * RT; ++e) {
-          const int pc = lane + 64 * e, sl = pc >> 1, Rw = sl / RT;
-          mine[u * 128 * RT + 2 * (sl ^ md_swz<RT>(Rw)) + (pc & 1)] = R.wv[u][e];
+          const int pc = lane + 64 * e, sl = pc >> 1, Rw = sl / RT, col = 16 * (sl % RT) + 8 * (pc & 1);
+          const int q = q0 + kMdWaves * u;
+          const bool live = col < r && q < nchunk && q * 64 + Rw < Kc;
+          mine[u * 128 * RT + 2 * (sl ^ md_swz<RT>(Rw)) + (pc & 1)] = live ? R.wv[u][e] : zero;
         }
 #pragma unroll
       for (int u = 0; u < GS; ++u)
@@ -209,22 +209,42 @@ __device__ __forceinline__ float md_sum(const f32x4* red, int row, int j) {
 
 }  // namespace
 
-// t (kBT false: in = x, W = A) or u (kBT true: in = dY, W = B), bf16 [M][rp]
-// with the ranks past r zero; rows without an adapter are not written. A block
-// of 16 rows takes one pass per adapter among its rows (rows of a request
-// follow each other, so mostly one); blockIdx.y deals the passes out.
+// s_a t (kBT false: in = x, W = A) or s_a u (kBT true: in = dY, W = B), rounded
+// to bf16 once, [M][rp] with the ranks past r zero; rows without an adapter are
+// not written. (One bf16 number each, as for a single adapter: the output is
+// bf16 itself. The scale goes in before the rounding, so that the GEMMs need
+// no scale.) A block of 16 rows takes one pass per adapter among its rows (rows
+// of a request follow each other, so mostly one); blockIdx.y deals the passes
+// out. Workgroups past `blocks` copy x into MFMA order: fragment (tile, ss, j)
+// has, at lane (g, c), columns 256 ss + 64 g + 8 j + (0 2 | 4 6 | 1 3 | 5 7)
+// of row 16 tile + c, zero past M and Kc.
 template <int RT, int GS, bool kBT>
-__global__ __launch_bounds__(64 * kMdWaves) void k_mdown(const uint16_t* in, int64_t M, int Kc, const uint16_t* W, int n,
-                                                         const int* __restrict__ index, int r, int rp,
-                                                         uint16_t* __restrict__ out) {
+__global__ __launch_bounds__(64 * kMdWaves) void k_mdown(const uint16_t* in, int64_t M, int Kc, const uint16_t* W,
+                                                         MultiLora ml, int r, int rp, uint16_t* __restrict__ out,
+                                                         unsigned blocks, u32x4* __restrict__ frags, int64_t nfrag) {
+  if (blockIdx.x >= blocks) {
+    if (kBT || blockIdx.y) return;
+    const int nss = (Kc + 255) / 256;
+    const int64_t f = static_cast<int64_t>(blockIdx.x - blocks) * kMdWaves + (threadIdx.x >> 6);
+    if (f >= nfrag) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t tile = f / (8 * nss);
+    const int rest = static_cast<int>(f - tile * 8 * nss);
+    const int64_t m = 16 * tile + (lane & 15);
+    const int k = 256 * (rest >> 3) + 64 * (lane >> 4) + 8 * (rest & 7);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (m < M && k < Kc) v = perm8(ld16(in + m * Kc + k));
+    frags[f * 64 + lane] = v;
+    return;
+  }
   constexpr int kPer = md_per<RT, GS, kBT>();
   __shared__ u32x4 lds[kMdWaves * kPer];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int c = lane & 15;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  int id = m0 + c < M ? index[m0 + c] : -1;
-  if (static_cast<unsigned>(id) >= static_cast<unsigned>(n)) id = -1;
+  int id = m0 + c < M ? ml.index[m0 + c] : -1;
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
   uint32_t pend = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
   for (unsigned ord = 0; pend; ++ord) {
@@ -237,11 +257,12 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(const uint16_t* in, int
                                     W + static_cast<int64_t>(a) * r * Kc, r, lds + w * kPer, acc, w, lane);
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) red[w * kPer + jt * 64 + lane] = acc[jt];
+    const float scale = ml.scale[a];
     __syncthreads();
     for (int e = t; e < 16 * rp; e += 64 * kMdWaves) {
       const int row = e / rp, j = e - row * rp;
       if (!((rows >> row) & 1)) continue;
-      out[(m0 + row) * rp + j] = j < 16 * RT ? bf16_bits(md_sum<RT, kPer>(red, row, j)) : uint16_t{0};
+      out[(m0 + row) * rp + j] = j < 16 * RT ? bf16_bits(scale * md_sum<RT, kPer>(red, row, j)) : uint16_t{0};
     }
     __syncthreads();
   }
@@ -582,23 +603,28 @@ __global__ __launch_bounds__(256) void k_mfinish(GradLists L, int items, const f
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t Kc, const uint16_t* W, int n,
-                             const int* index, int r, uint16_t* out, hipStream_t stream) {
+hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t Kc, const uint16_t* W,
+                             const MultiLora& ml, int r, uint16_t* out, hipStream_t stream, u32x4* frags,
+                             int64_t mtiles) {
   const int rp = static_cast<int>(rank_pad(r));
   const int64_t blocks = cdiv(M, 16);
-  // the passes of a block side by side while there are fewer blocks than about four per CU
-  int64_t y = 1024 / blocks;
-  if (y > n) y = n;
+  // the passes of a block side by side where that leaves at most one workgroup per CU
+  int64_t y = 256 / blocks;
+  if (y > ml.n) y = ml.n;
+  if (y > M) y = M;
   if (y > 16) y = 16;
   if (y < 1) y = 1;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y)), block(64 * kMdWaves);
+  const int64_t nfrag = frags ? mtiles * cdiv(Kc, 256) * 8 : 0;
+  const dim3 grid(static_cast<unsigned>(blocks + cdiv(nfrag, kMdWaves)), static_cast<unsigned>(y)), block(64 * kMdWaves);
   const int kc = static_cast<int>(Kc);
-#define QNF4_MD(RTV, GSV)                                                                                            \
-  do {                                                                                                               \
-    if (wrow)                                                                                                        \
-      hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RTV, GSV, false>), grid, block, 0, stream, in, M, kc, W, n, index, r, rp, out); \
-    else                                                                                                             \
-      hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RTV, GSV, true>), grid, block, 0, stream, in, M, kc, W, n, index, r, rp, out); \
+  const unsigned nb = static_cast<unsigned>(blocks);
+#define QNF4_MD1(RTV, GSV, BT)                                                                                         \
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RTV, GSV, BT>), grid, block, 0, stream, in, M, kc, W, ml, r, rp, out, nb, \
+                     frags, nfrag)
+#define QNF4_MD(RTV, GSV)                 \
+  do {                                    \
+    if (wrow) QNF4_MD1(RTV, GSV, false);  \
+    else QNF4_MD1(RTV, GSV, true);        \
   } while (0)
   switch (down_nt(r)) {
     case 1: QNF4_MD(1, 4); break;
@@ -607,6 +633,7 @@ hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t K
     default: QNF4_MD(8, 1); break;
   }
 #undef QNF4_MD
+#undef QNF4_MD1
   return hipGetLastError();
 }
 

@@ -437,7 +437,7 @@ int qlora_nf4_lora_fwd_multi(const uint16_t* x, int64_t M, int64_t N, int64_t K,
   if (st) return st;
   const qnf4::Codebook* cb = qnf4::codebook();
   if (!cb) return QLORA_ERR_INIT;
-  return hip_status(qnf4::launch_multi_fwd(x, M, N, K, packed, qscale, step, A, B, qnf4::MultiLora{index, scale, n}, r,
+  return hip_status(qnf4::launch_multi_fwd(x, M, N, K, packed, qscale, step, A, B, index, scale, n, r,
                                            y, workspace, *cb, as_stream(stream)));
 }
 
@@ -457,7 +457,7 @@ int qlora_nf4_bwd_dx_multi(const uint16_t* dy, int64_t M, int64_t N, int64_t K, 
   if (st) return st;
   const qnf4::Codebook* cb = qnf4::codebook();
   if (!cb) return QLORA_ERR_INIT;
-  return hip_status(qnf4::launch_multi_bwd(dy, M, N, K, packed, qscale, step, A, B, qnf4::MultiLora{index, scale, n}, r,
+  return hip_status(qnf4::launch_multi_bwd(dy, M, N, K, packed, qscale, step, A, B, index, scale, n, r,
                                            dx, workspace, *cb, as_stream(stream)));
 }
 

@@ -129,6 +129,9 @@ struct BScale4 {   // the same for the four steps of a super-step
 // columns 16 .. 31 are zero and skipped; else rank_pad(r) / 16), 0 for none.
 // kMulti: tab (one weight) has a pool B [n][N][r]; row m uses adapter
 // ml.index[m] of it; t carries the scale (`scale` is not used).
+// kMulti also splits K (ml.S > 1): workgroup p has tile p % tiles and range p /
+// tiles of the super-steps, adds the adapter term of the row blocks i with i %
+// S == range, and leaves fp32 partial sums (ml.part [S][M][N]) for k_split_sum.
 template <bool kQuad, int RSN, bool kMulti = false>
 __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, int rp, int r, float scale,
                                                      Codebook cb, MultiLora ml) {
@@ -148,7 +151,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
   // rows shared by weights with the same input stay in L2 across them).
   const int ntm = static_cast<int>(cdiv(M, kTile));
   int tm, tnv;
-  tile_of(blockIdx.x, ntm, tab.col0[tab.count], tm, tnv);
+  const int ntiles = ntm * tab.col0[tab.count];
+  const int split = kMulti ? __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x) / ntiles) : 0;
+  tile_of(blockIdx.x - split * ntiles, ntm, tab.col0[tab.count], tm, tnv);
   tm = __builtin_amdgcn_readfirstlane(tm);     // uniform already; this keeps the
   tnv = __builtin_amdgcn_readfirstlane(tnv);   // buffer descriptors in SGPRs
   int g = 0;
@@ -168,6 +173,8 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
   const int64_t m0 = static_cast<int64_t>(tm) * kTile, n0 = static_cast<int64_t>(tn) * kTile;
   const int64_t nk = K / 64;
   const int64_t nsup = (nk + 3) / 4;           // super-steps of four K steps
+  const int64_t sup0 = kMulti ? nsup * split / ml.S : 0, sup1 = kMulti ? nsup * (split + 1) / ml.S : nsup;
+  const int64_t kt0 = 4 * sup0;
 
   // x tile DMA (rows past M read as zero through the descriptor's range
   // check). Instruction i of wave w fills LDS rows 64w + 8i + (lane >> 3),
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
   using U3 = std::integral_constant<int, 3>;
   auto decode_step0 = [&](auto&& scale0) {
     u32x4 c0[2];
-    read_codes(0, c0);
+    read_codes(kt0, c0);
     bf16x8 (&bo)[2][4] = B0_;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -347,20 +354,20 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
   // relied on to cover reads at other offsets of the slab.
   if constexpr (kQuad) {
     BScale4 Qc, Qn;
-    load_s4(0, Qc);
+    load_s4(sup0, Qc);
     __builtin_amdgcn_sched_barrier(0);
-    dma_a(0, As0);
+    dma_a(kt0, As0);
     __builtin_amdgcn_sched_barrier(0);
-    dma_b(0);
+    dma_b(sup0);
     __builtin_amdgcn_sched_barrier(0);
-    dma_a(imin(1, nk - 1), As1);
+    dma_a(imin(kt0 + 1, nk - 1), As1);
     __builtin_amdgcn_sched_barrier(0);
-    dma_a(imin(2, nk - 1), As2);
+    dma_a(imin(kt0 + 2, nk - 1), As2);
     __builtin_amdgcn_sched_barrier(0);
     wait_vm<16>();                             // scales of super-step 0, x tile 0, code slab 0
-    decode_step0([&](int j) { return scale_of(Qc, 0, 0, j); });
+    decode_step0([&](int j) { return scale_of(Qc, 0, kt0, j); });
     lds_barrier();
-    for (int64_t S = 0; S < nsup; ++S) {
+    for (int64_t S = sup0; S < sup1; ++S) {
       const int64_t k = 4 * S;
       step_k(U0{}, As0, As3, B0, B1, nothing, [&](int j) { return scale_of(Qc, 1, k + 1, j); }, k);
       wait_vm<16>();
@@ -379,17 +386,17 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
     }
   } else {
     BScale P0, P1;
-    dma_a(0, As0);
+    dma_a(kt0, As0);
     __builtin_amdgcn_sched_barrier(0);
-    dma_b(0);
+    dma_b(sup0);
     __builtin_amdgcn_sched_barrier(0);
-    dma_a(imin(1, nk - 1), As1);
+    dma_a(imin(kt0 + 1, nk - 1), As1);
     __builtin_amdgcn_sched_barrier(0);
-    load_s(0, P0);
+    load_s(kt0, P0);
     __builtin_amdgcn_sched_barrier(0);
-    dma_a(imin(2, nk - 1), As2);
+    dma_a(imin(kt0 + 2, nk - 1), As2);
     __builtin_amdgcn_sched_barrier(0);
-    load_s(1, P1);
+    load_s(kt0 + 1, P1);
     __builtin_amdgcn_sched_barrier(0);
     wait_vm<12>();                             // everything up to the scales of step 0
     // pin step 1's scales here: left alone, the (read-only) loads get sunk
@@ -398,7 +405,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
     decode_step0([&](int j) { return block_scale(P0.q[j], P0.d[j]) * P0.live; });
     lds_barrier();
     auto sc = [](const BScale& P, int j) { return block_scale(P.q[j], P.d[j]) * P.live; };
-    for (int64_t S = 0; S < nsup; ++S) {
+    for (int64_t S = sup0; S < sup1; ++S) {
       const int64_t k = 4 * S;
       step_k(U0{}, As0, As3, B0, B1, [&] { load_s(k + 2, P0); }, [&](int j) { return sc(P1, j); }, k);
       wait_vm<28>();
@@ -455,72 +462,121 @@ __global__ __launch_bounds__(256, 1) void k_gemm_fwd(FwdTable tab, int64_t M, in
           }
       }
     };
-    // a pool of adapters: block by block of 32 rows, the adapters among them
-    // (mostly one: rows of a request follow each other); an adapter's B
-    // fragments are kept until another one is needed. The sums of a block are
-    // added once, outside the loop over its adapters, so that the
-    // accumulators stay where they are. t carries the scale.
-    auto lora_multi = [&](auto rsn_c) {
-      constexpr int RS = decltype(rsn_c)::value;
-      constexpr int IG = RS <= 2 ? 8 : RS <= 4 ? 4 : 2;
-      TileRows tr;
-      tr.init(ml, m0, M, lane);
-      u32x4 bfr[2][RS];
-      int have = -1;
+    if constexpr (!kMulti) lora(std::integral_constant<int, RSN>{});
+  }
+  // A pool of adapters: block by block of 32 rows, the adapters among them
+  // (mostly one: rows of a request follow each other), then the block's
+  // stores. The loop stays rolled: unrolled over the eight blocks, its branches
+  // cost 230 to 740 bytes of spills a lane and 70 to 130 KB of code, twice the
+  // instruction cache. An adapter's B fragments are kept until another one is
+  // needed; t carries the scale. Rows are chosen after the product.
+  if constexpr (kMulti) {
+    constexpr int RS = RSN;
+    const bool vec_ok = (r & 7) == 0;
+    TileRows tr;
+    tr.init(ml, m0, M, lane);
+    u32x4 bfr[2][RS], tf[RS], tn[RS];
+    auto load_t = [&](int i, u32x4 (&f)[RS]) {
+      const int64_t mrow = imin(m0 + 32 * i + l32, M - 1);
 #pragma unroll
-      for (int i0 = 0; i0 < 8; i0 += IG) {
-        u32x4 tf[IG][RS];
+      for (int rs = 0; rs < RS; ++rs) f[rs] = ld16(tl + mrow * rp + 16 * rs + 8 * h);
+    };
+    load_t(0, tn);
+    int have = -1;
+    const bool wide = n0 + kTile <= N && N % 8 == 0;
+    uint16_t* const yl = reinterpret_cast<uint16_t*>(Bw);      // the wave's slab: 32 rows x 64 columns, chunks swizzled by row
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
 #pragma unroll
-        for (int ii = 0; ii < IG; ++ii) {
-          const int64_t mrow = imin(m0 + 32 * (i0 + ii) + l32, M - 1);
+      for (int rs = 0; rs < RS; ++rs) tf[rs] = tn[rs];
+      load_t(i < 7 ? i + 1 : 7, tn);
+      f32x16 cur[2];
+      switch (i) {
+        case 0: cur[0] = acc[0][0], cur[1] = acc[0][1]; break;
+        case 1: cur[0] = acc[1][0], cur[1] = acc[1][1]; break;
+        case 2: cur[0] = acc[2][0], cur[1] = acc[2][1]; break;
+        case 3: cur[0] = acc[3][0], cur[1] = acc[3][1]; break;
+        case 4: cur[0] = acc[4][0], cur[1] = acc[4][1]; break;
+        case 5: cur[0] = acc[5][0], cur[1] = acc[5][1]; break;
+        case 6: cur[0] = acc[6][0], cur[1] = acc[6][1]; break;
+        default: cur[0] = acc[7][0], cur[1] = acc[7][1]; break;
+      }
+      const int id = i < 2 ? tr.id[0] : i < 4 ? tr.id[1] : i < 6 ? tr.id[2] : tr.id[3];
+      const int up = 32 * (i & 1);
+      uint32_t pend = i % ml.S == split ? static_cast<uint32_t>(__ballot(id >= 0) >> up) : 0u;
+      if (pend) {
+        f32x16 tmp[2];
 #pragma unroll
-          for (int rs = 0; rs < RS; ++rs) tf[ii][rs] = ld16(tl + mrow * rp + 16 * rs + 8 * h);
-        }
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int ii = 0; ii < IG; ++ii) {
-          const int i = i0 + ii;
-          const int id = tr.id[i >> 1];
-          uint64_t pend = __ballot(id >= 0) & (0xFFFFFFFFull << (32 * (i & 1)));
-          f32x16 tmp[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) tmp[j][v] = 0.f;
-          while (pend) {
-            const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(pend));
-            const uint64_t rows = __ballot(id == a) & pend;
-            pend &= ~rows;
-            if (a != have) {
-              have = a;
-              const uint16_t* Ba = Bl + static_cast<int64_t>(a) * N * r;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int64_t nrow = imin(n0 + 64 * w + 32 * j + l32, N - 1);
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs) bfr[j][rs] = load_row8(Ba + nrow * r, 16 * rs + 8 * h, r, vec_ok);
-              }
-            }
+          for (int v = 0; v < 16; ++v) tmp[j][v] = 0.f;
+        while (pend) {
+          const int a = __builtin_amdgcn_readlane(id, up + __builtin_ctz(pend));
+          const uint32_t rows = static_cast<uint32_t>(__ballot(id == a) >> up);
+          pend &= ~rows;
+          if (a != have) {
+            have = a;
+            const uint16_t* Ba = Bl + static_cast<int64_t>(a) * N * r;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              f32x16 p;
+              const uint16_t* Br = Ba + imin(n0 + 64 * w + 32 * j + l32, N - 1) * r;
 #pragma unroll
-              for (int v = 0; v < 16; ++v) p[v] = 0.f;
-#pragma unroll
-              for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(tf[ii][rs]), as_bf16x8(bfr[j][rs]), p);
-              take_rows(tmp[j], p, static_cast<uint32_t>(rows >> (32 * (i & 1))), h);
+              for (int rs = 0; rs < RS; ++rs) bfr[j][rs] = load_row8(Br, 16 * rs + 8 * h, r, vec_ok);
             }
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j) {
+            f32x16 p;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] += tmp[j][v];
+            for (int v = 0; v < 16; ++v) p[v] = 0.f;
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(tf[rs]), as_bf16x8(bfr[j][rs]), p);
+            take_rows(tmp[j], p, rows, h);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) cur[j][v] += tmp[j][v];
       }
-    };
-    if constexpr (kMulti)
-      lora_multi(std::integral_constant<int, RSN>{});
-    else
-      lora(std::integral_constant<int, RSN>{});
+      const int64_t mb = m0 + 32 * i;
+      if (ml.S > 1) {
+        float* const pt = ml.part + (split * M + mb) * N + n0 + 64 * w + l32;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int row = 8 * (v >> 2) + 4 * h + (v & 3);
+            if (mb + row < M && n0 + 64 * w + 32 * j + l32 < N) pt[row * N + 32 * j] = cur[j][v];
+          }
+      } else if (wide) {
+        // through the wave's slab to whole 128-byte rows
+        wait_lgkm0();
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int row = 8 * (v >> 2) + 4 * h + (v & 3), col = 32 * j + l32;
+            yl[row * 64 + 8 * ((col >> 3) ^ (row & 7)) + (col & 7)] = bf16_bits(cur[j][v]);
+          }
+        wait_lgkm0();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 8 * e + (lane >> 3), ch = lane & 7;
+          const u32x4 o = Bw[row * 8 + (ch ^ (row & 7))];
+          if (mb + row < M) *reinterpret_cast<u32x4*>(y + (mb + row) * N + n0 + 64 * w + 8 * ch) = o;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int64_t mm = mb + 8 * (v >> 2) + 4 * h + (v & 3), nn = n0 + 64 * w + 32 * j + l32;
+            if (mm < M && nn < N) y[mm * N + nn] = bf16_bits(cur[j][v]);
+          }
+      }
+    }
+    return;
   }
   // bf16 stores: for fixed (i, j, v) the 32 lanes of a half-wave write 64
   // contiguous bytes of one row; interior tiles skip the bounds checks
@@ -581,7 +637,9 @@ struct BCodes {
 };
 
 // RSN: rank chunks of 16 in the LoRA epilogue (1 for r <= 16, else rank_pad(r) / 16), 0 for none.
-// kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m]; u carries the scale.
+// kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m]; u carries the
+// scale. It also splits the contraction (ml.S > 1) as k_gemm_fwd does, in ranges
+// of whole step pairs; the o-th adapter of a tile is added by range o % S.
 template <int RSN, bool kMulti = false>
 __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __restrict__ dy, int64_t M, int64_t N,
                                                             int64_t K, const uint8_t* __restrict__ packed,
@@ -604,12 +662,15 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   const int h = lane >> 5, l32 = lane & 31;
   const int ntm = static_cast<int>(cdiv(M, kTile)), ntk = static_cast<int>(cdiv(K, kTile));
   int tm, tk;
-  tile_of(blockIdx.x, ntm, ntk, tm, tk);
+  const int split = kMulti ? __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x) / (ntm * ntk)) : 0;
+  tile_of(blockIdx.x - split * ntm * ntk, ntm, ntk, tm, tk);
   tm = __builtin_amdgcn_readfirstlane(tm);
   tk = __builtin_amdgcn_readfirstlane(tk);
   const int64_t m0 = static_cast<int64_t>(tm) * kTile, k0 = static_cast<int64_t>(tk) * kTile;
   const int64_t nbr = K / 64;
-  const int64_t nsteps = cdiv(N, 64);
+  const int64_t nsteps = cdiv(N, 64), npairs = (nsteps + 1) / 2;
+  const int64_t st0 = kMulti ? 2 * (npairs * split / ml.S) : 0;
+  const int64_t st1 = kMulti ? 2 * (npairs * (split + 1) / ml.S) : nsteps;
 
   // dY tile staging through registers (not LDS DMA: the transposed LDS reads
   // of W' carry no alias information, so any LDS DMA in flight would make the
@@ -732,13 +793,17 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
     }
   };
 
+  // a pool's rows: asked for here, used in the epilogue
+  TileRows tr;
+  if constexpr (kMulti) tr.init(ml, m0, M, lane);
+
   // prologue: dY tile 0, codes of steps 0 and 1; decode step 0
   BCodes P0, P1;
-  load_a(0);
+  load_a(st0);
   __builtin_amdgcn_sched_barrier(0);
-  load_codes(0, P0);
+  load_codes(st0, P0);
   __builtin_amdgcn_sched_barrier(0);
-  load_codes(1, P1);
+  load_codes(st0 + 1, P1);
   __builtin_amdgcn_sched_barrier(0);
   store_a(As0);
   asm volatile("" ::"v"(P1.p), "v"(static_cast<int>(P1.q)), "v"(P1.d));
@@ -752,7 +817,7 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   // The end of step st waits for this wave's LDS writes (W' and dY of step
   // st+1), then the barrier publishes them; the code loads of step st+2 stay
   // in flight.
-  for (int64_t st = 0; st < nsteps; st += 2) {
+  for (int64_t st = st0; st < st1; st += 2) {
     step_b(As0, As1, Ws0, Ws1, P1, P0, st);
     __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
     lds_barrier();
@@ -826,12 +891,22 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
     // stay where they are. u carries the scale.
     auto lora_multi = [&](auto rsn_c) {
       constexpr int RS = decltype(rsn_c)::value;
-      TileRows tr;
-      tr.init(ml, m0, M, lane);
       uint64_t pend[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) pend[q] = __ballot(tr.id[q] >= 0);
-      while (pend[0] | pend[1] | pend[2] | pend[3]) {
+      // u of the wave's rows once, where it fits the registers
+      constexpr bool kKeep = RS <= 2;
+      u32x4 uf[kKeep ? 4 : 1][RS];
+      auto load_u = [&](int i, u32x4 (&f)[RS]) {
+        const int64_t mrow = imin(m0 + 128 * wm + 32 * i + l32, M - 1);
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs) f[rs] = ld16(ul + mrow * rp + 16 * rs + 8 * h);
+      };
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_u(i, uf[i]);
+      }
+      for (int ord = 0; pend[0] | pend[1] | pend[2] | pend[3]; ++ord) {
         const int a = pend[0]   ? __builtin_amdgcn_readlane(tr.id[0], __builtin_ctzll(pend[0]))
                       : pend[1] ? __builtin_amdgcn_readlane(tr.id[1], __builtin_ctzll(pend[1]))
                       : pend[2] ? __builtin_amdgcn_readlane(tr.id[2], __builtin_ctzll(pend[2]))
@@ -842,6 +917,7 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
           rows[q] = __ballot(tr.id[q] == a);
           pend[q] &= ~rows[q];
         }
+        if (ord % ml.S != split) continue;
         __syncthreads();                       // the reads of the slice before (or of the last W' tile)
         stage_a(Al + static_cast<int64_t>(a) * r * K);
         __syncthreads();
@@ -849,17 +925,14 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t rm = static_cast<uint32_t>((i < 2 ? r0 : r1) >> (32 * (i & 1)));
-          u32x4 uf[RS];
-          const int64_t mrow = imin(m0 + 128 * wm + 32 * i + l32, M - 1);
-#pragma unroll
-          for (int rs = 0; rs < RS; ++rs) uf[rs] = ld16(ul + mrow * rp + 16 * rs + 8 * h);
+          if constexpr (!kKeep) load_u(i, uf[0]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             f32x16 p, tmp;
 #pragma unroll
             for (int v = 0; v < 16; ++v) p[v] = tmp[v] = 0.f;
 #pragma unroll
-            for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(uf[rs]), read_bj(Ws, rs, j), p);
+            for (int rs = 0; rs < RS; ++rs) p = mfma32(as_bf16x8(uf[kKeep ? i : 0][rs]), read_bj(Ws, rs, j), p);
             take_rows(tmp, p, rm, h);
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] += tmp[v];
@@ -875,6 +948,21 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
       stage_a(Al);
       __syncthreads();
       lora(std::integral_constant<int, RSN>{});
+    }
+  }
+  if constexpr (kMulti) {
+    if (ml.S > 1) {
+      float* const pt = ml.part + (split * M + m0 + 128 * wm) * K + k0 + 64 * wn + l32;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+            if (m0 + 128 * wm + row < M && k0 + 64 * wn + 32 * j + l32 < K) pt[row * K + 32 * j] = acc[i][j][v];
+          }
+      return;
     }
   }
   if (m0 + kTile <= M && k0 + kTile <= K) {
@@ -1048,23 +1136,97 @@ hipError_t launch_bwd_dx(const uint16_t* dy, int64_t M, int64_t N, int64_t K, co
 }
 
 // ---------------------------------------------------------------------------
-// a pool of adapters: t or u of every row (launch_multi_down), then the tiled
-// GEMM with the row-by-row epilogue
+// a pool of adapters: t or u of every row (launch_multi_down), then the
+// streaming forward, or the tiled GEMM with the row-by-row epilogue
 // ---------------------------------------------------------------------------
+// out[i] = bf16(sum of the S partials of element i, in order), 8 per thread;
+// count is a multiple of 8 or the rest goes one by one
+__global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ part, int S, int64_t count,
+                                                   uint16_t* __restrict__ out) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= count) return;
+  if (i + 8 <= count && count % 4 == 0) {
+    f32x4 a = *reinterpret_cast<const f32x4*>(part + i), b = *reinterpret_cast<const f32x4*>(part + i + 4);
+    for (int s = 1; s < S; ++s) {
+      a += *reinterpret_cast<const f32x4*>(part + s * count + i);
+      b += *reinterpret_cast<const f32x4*>(part + s * count + i + 4);
+    }
+    *reinterpret_cast<u32x4*>(out + i) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                               pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+    return;
+  }
+  for (int64_t e = i; e < i + 8 && e < count; ++e) {
+    float sum = part[e];
+    for (int s = 1; s < S; ++s) sum += part[s * count + e];
+    out[e] = bf16_bits(sum);
+  }
+}
+
+// How a call of op 0 (forward, contraction over K) or 1 (backward, over N) runs.
+// The contraction of the tiled kernels is split while the tiles leave CUs
+// idle: into S ranges of at least two super-steps (forward, 256 deep) or eight
+// steps (backward, 64 deep). The time of each way, in us, from the shapes
+// measured:
+//   tiled      ranges of 64-deep steps at 1.4 each, 8 to start and end, and the
+//              partial sums written and read at 4 TB/s and another launch
+//   streaming  rounds of items; an item is 9 and 2.8 per super-step of a wave
+// e.g. 700 rows at 4096 x 11008: streaming 127 (3 rounds), tiled in five ranges
+// 88; 256 rows at 4096 x 4096: streaming 24, tiled 38.
+struct MultiPlan {
+  bool stream = false;
+  int64_t S = 1;
+  size_t t_off = 0, down_off = 0, part_off = 0, total = 0;   // the tiled kernels' workspace
+};
+static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
+  MultiPlan p;
+  const int64_t Kc = op == 0 ? K : N, cols = op == 0 ? N : K;
+  const int64_t tiles = cdiv(M, kTile) * cdiv(cols, kTile), steps = cdiv(Kc, 64);
+  double best = 0;
+  for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 8)); ++S) {
+    double us = static_cast<double>(cdiv(S * tiles, 256)) * (1.4 * 4 * cdiv(cdiv(steps, 4), S) + 8);
+    if (S > 1) us += 4 + 8e-6 * static_cast<double>(S * M * cols) / 4;
+    if (S == 1 || us < best) best = us, p.S = S;
+  }
+  if (op == 0 && M <= kMsMaxM) {
+    const MsPlan m = ms_plan(M, N, K, r, n);
+    const int64_t items = cdiv(N, 64) * m.mblocks * m.S;
+    const double us = static_cast<double>(cdiv(items, m.MT <= 2 ? 512 : 256)) * (9 + 2.8 * cdiv(cdiv(K, 256), 4 * m.S));
+    if (us <= best) {
+      p.stream = true;
+      p.total = m.total;
+      return p;
+    }
+  }
+  p.t_off = kWsCounterBytes;
+  p.down_off = p.t_off + align256(static_cast<size_t>(M * rank_pad(r) * 2));
+  p.part_off = p.down_off + multi_down_plan(M, Kc, r, n).part_bytes;
+  p.total = p.part_off + (p.S > 1 ? align256(static_cast<size_t>(p.S * M * cols) * 4) : 0);
+  return p;
+}
+
 size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
-  if (op == 2) return multi_grad_plan(M, N, K, r, n, true).total;
-  if (op == 0 && M <= kMsMaxM) return ms_plan(M, N, K, r).total;
-  return kWsCounterBytes + align256(static_cast<size_t>(M * rank_pad(r) * 2));
+  return op == 2 ? multi_grad_plan(M, N, K, r, n, true).total : multi_plan(op, M, N, K, r, n).total;
+}
+
+static hipError_t launch_split_sum(const MultiLora& ml, int64_t count, uint16_t* out, hipStream_t stream) {
+  if (ml.S > 1)
+    hipLaunchKernelGGL(k_split_sum, dim3(static_cast<unsigned>(cdiv(count, 2048))), dim3(256), 0, stream, ml.part, ml.S,
+                       count, out);
+  return hipGetLastError();
 }
 
 hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
-                            const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,
-                            hipStream_t stream) {
-  if (M <= kMsMaxM)
-    return launch_mstream(ms_plan(M, N, K, r), x, M, N, K, packed, qscale, step, A, B, ml, r, y, ws, cb, stream);
-  uint16_t* tl = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
-  const hipError_t e = launch_multi_down(true, x, M, K, A, ml, r, tl, stream);
+                            const int* index, const float* scale, int n, int r, uint16_t* y, void* ws,
+                            const Codebook& cb, hipStream_t stream) {
+  const MultiPlan p = multi_plan(0, M, N, K, r, n);
+  char* wsb = static_cast<char*>(ws);
+  const MultiLora ml{index, scale, n, static_cast<int>(p.S), reinterpret_cast<float*>(wsb + p.part_off)};
+  if (p.stream)
+    return launch_mstream(ms_plan(M, N, K, r, n), x, M, N, K, packed, qscale, step, A, B, ml, r, y, ws, cb, stream);
+  uint16_t* tl = reinterpret_cast<uint16_t*>(wsb + p.t_off);
+  const hipError_t e = launch_multi_down(true, x, M, K, A, ml, r, tl, ws, reinterpret_cast<float*>(wsb + p.down_off),
+                                         stream);
   if (e != hipSuccess) return e;
   const int rp = static_cast<int>(rank_pad(r));
   FwdTable tab{};
@@ -1079,7 +1241,7 @@ hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, 
   tab.N[0] = static_cast<int>(N);
   tab.K[0] = static_cast<int>(K);
   tab.col0[1] = static_cast<int>(cdiv(N, kTile));
-  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(N, kTile)));
+  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(N, kTile) * p.S));
 #define QNF4_MFWD(RSNV)                                                                                        \
   do {                                                                                                         \
     if (K % 256 == 0)                                                                                          \
@@ -1099,18 +1261,22 @@ hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, 
   }
 #undef QNF4_MFWD
   mark_kernel(1, stream);
-  return hipGetLastError();
+  return launch_split_sum(ml, M * N, y, stream);
 }
 
 hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
-                            const MultiLora& ml, int r, uint16_t* dx, void* ws, const Codebook& cb,
-                            hipStream_t stream) {
-  uint16_t* ul = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kWsCounterBytes);
-  const hipError_t e = launch_multi_down(false, dy, M, N, B, ml, r, ul, stream);
+                            const int* index, const float* scale, int n, int r, uint16_t* dx, void* ws,
+                            const Codebook& cb, hipStream_t stream) {
+  const MultiPlan p = multi_plan(1, M, N, K, r, n);
+  char* wsb = static_cast<char*>(ws);
+  const MultiLora ml{index, scale, n, static_cast<int>(p.S), reinterpret_cast<float*>(wsb + p.part_off)};
+  uint16_t* ul = reinterpret_cast<uint16_t*>(wsb + p.t_off);
+  const hipError_t e = launch_multi_down(false, dy, M, N, B, ml, r, ul, ws, reinterpret_cast<float*>(wsb + p.down_off),
+                                         stream);
   if (e != hipSuccess) return e;
   const int rp = static_cast<int>(rank_pad(r));
-  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(K, kTile)));
+  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(K, kTile) * p.S));
 #define QNF4_MBWD(RSNV)                                                                                       \
   hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_bwd<RSNV, true>), grid, dim3(kBwThreads), 0, stream, dy, M, N, K, packed, \
                      qscale, step, static_cast<const uint16_t*>(ul), rp, A, r, 0.0f, dx, cb, ml)
@@ -1124,7 +1290,7 @@ hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K,
   }
 #undef QNF4_MBWD
   mark_kernel(1, stream);
-  return hipGetLastError();
+  return launch_split_sum(ml, M * K, dx, stream);
 }
 
 size_t bwd_batched_ws_bytes(int64_t M, int G, const int64_t* N, const int64_t* K, int r) {

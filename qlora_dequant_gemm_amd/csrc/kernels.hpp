@@ -248,16 +248,18 @@ struct MultiLora {
   const int* index;         // [M]
   const float* scale;       // [n]
   int n;
+  int S;                    // ranges of a split contraction (tiled kernels)
+  float* part;              // S > 1: fp32 partial sums [S][M][columns]
 };
 
 hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
-                            const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb,
-                            hipStream_t stream);
+                            const int* index, const float* scale, int n, int r, uint16_t* y, void* ws,
+                            const Codebook& cb, hipStream_t stream);
 hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                             const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
-                            const MultiLora& ml, int r, uint16_t* dx, void* ws, const Codebook& cb,
-                            hipStream_t stream);
+                            const int* index, const float* scale, int n, int r, uint16_t* dx, void* ws,
+                            const Codebook& cb, hipStream_t stream);
 size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n);
 
 // Gradients: the rows of each adapter listed in chunks of 64 places (a place
@@ -279,8 +281,9 @@ struct GradLists {
 struct MultiGradPlan {
   int nt = 1;               // rank tiles of 16 (a power of two)
   int64_t chunks = 0, Mp = 0, per_item = 1, items = 0, slots = 0;   // chunks, items and slots at most
+  int64_t S = 1;            // splits of the products t and u
   size_t rows_off = 0, chunk_off = 0, item_off = 0, adapter_off = 0, total_off = 0;
-  size_t tt_off = 0, ut_off = 0, pa_off = 0, pb_off = 0, total = 0;
+  size_t tt_off = 0, ut_off = 0, dp_off = 0, pa_off = 0, pb_off = 0, total = 0;
 };
 MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, bool listed);
 // xfmt: kActBf16 (x bf16), or the format of a checkpoint (x its codes, tops its

@@ -102,6 +102,14 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
       for (int j = 0; j < 4; ++j) x[j][i] = xs[64 * j];
     }
   };
+  // the rows' adapters, asked for now and used at the end
+  int id[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = 16 * (mt0 + i) + c;
+    id[i] = m < P.M ? ml.index[m] : -1;
+    if (static_cast<unsigned>(id[i]) >= static_cast<unsigned>(ml.n)) id[i] = -1;
+  }
   f32x4 acc[kMsNT][MT];
 #pragma unroll
   for (int nt = 0; nt < kMsNT; ++nt)
@@ -169,9 +177,7 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
     for (int i = 0; i < MT; ++i) {
       if ((mt0 + i) % P.S != s) continue;
       const int m = 16 * (mt0 + i) + c;
-      int id = m < P.M ? ml.index[m] : -1;
-      if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
-      uint32_t pend = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
+      uint32_t pend = static_cast<uint32_t>(__ballot(id[i] >= 0)) & 0xFFFFu;
       if (!pend) continue;
       const uint16_t* trow = P.t + static_cast<int64_t>(m < P.M ? m : P.M - 1) * rp;
       f32x4 lora = {0.f, 0.f, 0.f, 0.f};
@@ -180,8 +186,8 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
         int ad[kMsBatch];
 #pragma unroll
         for (int u = 0; u < kMsBatch; ++u) {
-          ad[u] = __builtin_amdgcn_readlane(id, pend ? __builtin_ctz(pend) : 0);
-          rows[u] = pend ? static_cast<uint32_t>(__ballot(id == ad[u])) & 0xFFFFu : 0u;
+          ad[u] = __builtin_amdgcn_readlane(id[i], pend ? __builtin_ctz(pend) : 0);
+          rows[u] = pend ? static_cast<uint32_t>(__ballot(id[i] == ad[u])) & 0xFFFFu : 0u;
           pend &= ~rows[u];
         }
         f32x4 p[kMsBatch];
@@ -287,18 +293,20 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
 }  // namespace
 
 // Items: blocks of 64 weight rows x blocks of 16 MT rows of x (MT up to 4) x S
-// ranges of K; S fills the chip with about two workgroups per CU while every
-// wave still gets a super-step.
-MsPlan ms_plan(int64_t M, int64_t N, int64_t K, int r) {
+// ranges of K. S is the most that keeps every item resident at once (two
+// workgroups per CU up to MT = 2, one above; a second round costs a whole item:
+// 48 rows at 11008 x 4096 take 21 us with S = 1, 29 with 2, 35 with 3) and
+// leaves every wave a super-step.
+MsPlan ms_plan(int64_t M, int64_t N, int64_t K, int r, int n) {
   MsPlan p;
   const int64_t mtiles = cdiv(M, 16), nss = cdiv(K, 256);
   p.MT = static_cast<int>(mtiles < 4 ? mtiles : 4);
   p.mblocks = cdiv(mtiles, p.MT);
   const int64_t blocks = cdiv(N, kMsRows) * p.mblocks;
-  int64_t S = cdiv(512, blocks);
+  int64_t S = (p.MT <= 2 ? 512 : 256) / blocks;
   if (S > cdiv(nss, 4)) S = cdiv(nss, 4);
   if (S > kMsMaxSplit) S = kMsMaxSplit;
-  p.S = blocks >= 384 ? 1 : S;
+  p.S = S < 1 ? 1 : S;
   size_t off = kWsCounterBytes;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -307,6 +315,7 @@ MsPlan ms_plan(int64_t M, int64_t N, int64_t K, int r) {
   };
   p.t_off = take(static_cast<size_t>(M * rank_pad(r) * 2));
   p.x_off = take(static_cast<size_t>(p.mblocks * p.MT * nss) * 8192);
+  p.down_off = take(multi_down_plan(M, K, r, n).part_bytes);
   p.part_off = take(p.S > 1 ? static_cast<size_t>(blocks * p.S) * 16 * p.MT * kMsRows * 4 : 0);
   p.total = off;
   return p;
@@ -318,7 +327,8 @@ hipError_t launch_mstream(const MsPlan& p, const uint16_t* x, int64_t M, int64_t
   char* wsb = static_cast<char*>(ws);
   uint16_t* t = reinterpret_cast<uint16_t*>(wsb + p.t_off);
   u32x4* xp = reinterpret_cast<u32x4*>(wsb + p.x_off);
-  const hipError_t e = launch_multi_down(true, x, M, K, A, ml, r, t, stream, xp, p.mblocks * p.MT);
+  const hipError_t e = launch_multi_down(true, x, M, K, A, ml, r, t, ws, reinterpret_cast<float*>(wsb + p.down_off), stream,
+                                         xp, p.mblocks * p.MT);
   if (e != hipSuccess) return e;
   MsArgs a{};
   a.xp = xp;

@@ -10,8 +10,8 @@
 //     dB_a = s_a sum_m dY_m^T t_m,   dA_a = s_a sum_m u_m^T x_m   (rows m of a)
 //
 // k_mdown  s_a t or s_a u of a batch in its own order, for the forward and
-//          backward GEMMs: 16 rows per workgroup, one pass per adapter among
-//          them; beside it, x in MFMA order for the streaming forward.
+//          backward GEMMs: 16 or 64 rows per workgroup, one pass per adapter
+//          among them; beside it, x in MFMA order for the streaming forward.
 // The gradients first list each adapter's rows (k_msort: the rows of an adapter in
 // batch order, padded to whole 64-row chunks), so that every later product has
 // one adapter per chunk and needs no masks:
@@ -30,6 +30,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "act8.hpp"
 #include "mm_common.hpp"
 #include "multi.hpp"
@@ -41,144 +43,181 @@ namespace {
 constexpr int kMdWaves = 8;
 constexpr int kSplit = 3;                      // bf16 numbers that carry one fp32 value of t or u
 
-// The transposed LDS copy of 64 adapter rows (B [Kc][r]): 32-byte pieces (row
-// R, rank tile jt) at (R RT + jt) ^ swz(R), so that 16-byte writes and
-// ds_read_b64_tr_b16 both touch 64 distinct banks (as in lora.hip).
+// A wave takes at most two rank tiles of 16 (its registers), so the eight waves
+// are (8 / groups) shares of the contraction x groups of rank tiles.
 template <int RT>
+constexpr int md_rtw() { return RT < 2 ? RT : 2; }
+template <int RT>
+constexpr int md_groups() { return RT / md_rtw<RT>(); }
+
+// The transposed LDS copy of 64 adapter rows (B [Kc][r], the wave's ranks):
+// 32-byte pieces (row R, rank tile jt) at (R RTW + jt) ^ swz(R), so that
+// 16-byte writes and ds_read_b64_tr_b16 both touch 64 distinct banks (as in
+// lora.hip).
+template <int RTW>
 __device__ __forceinline__ int md_swz(int R) {
-  if constexpr (RT == 1) return ((R >> 4) & 1) << 2;
-  else if constexpr (RT == 2) return (R >> 4) & 1;
-  else if constexpr (RT == 4) return ((R >> 1) & 1) | (((R >> 4) & 1) << 1);
-  else return (R & 3) | (((R >> 4) & 1) << 2);
+  if constexpr (RTW == 1) return ((R >> 4) & 1) << 2;
+  else return (R >> 4) & 1;
 }
 
-// LDS chunks (16 bytes) a wave needs: its staged adapter rows, then its sums
-template <int RT, int GS, bool kBT>
-constexpr int md_per() {
-  constexpr int stage = kBT ? GS * 128 * RT : 0;
-  return stage > 64 * RT ? stage : 64 * RT;
+// 64-deep chunks of a round (all their loads go out together); two rounds are
+// in registers
+template <int RM, int RTW>
+constexpr int md_gs() {
+  if constexpr (RM == 1) return RTW == 1 ? 4 : 2;
+  else return RTW == 1 ? 2 : 1;
+}
+// LDS chunks (16 bytes) of a workgroup: the waves' staged adapter rows, or
+// their sums of one rank tile
+template <int RM, int RT, bool kBT>
+constexpr int md_lds() {
+  constexpr int stage = kBT ? md_gs<RM, md_rtw<RT>()>() * 128 * md_rtw<RT>() : 0;
+  return kMdWaves * (stage > 64 * RM ? stage : 64 * RM);
 }
 
-// 16 rows x 16 RT ranks of (rows of `in`) . W^T, this wave's share of the
-// contraction: chunks w, w + 8, ... of 64. Lane (g, c) supplies 16 elements
-// of its row (`row`, < 0: zeros) at 16 g of each chunk. kBT: W is B [Kc][r],
-// else A [r][Kc]. XF: the format of `in` (kActBf16 or a checkpoint with one
-// constant per 64 values in `tops`). Pieces past Kc, ranks past r and absent
-// rows are zero on both sides, whatever the memory next to them holds.
-template <int RT, int GS, bool kBT, int XF>
-__device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, int64_t row, int Kc,
-                                         const uint16_t* W, int r, u32x4* mine, f32x4 (&acc)[RT], int w, int lane) {
+// This wave's share of the product of 16 RM rows of `in` with the adapter W
+// (kBT: B [Kc][r], else A [r][Kc]) over the 64-deep chunks [qb, qe): chunks qb +
+// w, qb + w + 8, ... Lane (g, c) supplies 16 elements at 16 g of each chunk of
+// row rows[i] of tile i. XF: the format of `in` (kActBf16, or a checkpoint with
+// one constant per 64 values in `tops`). An absent row (< 0) repeats row 0 and a
+// rank past r repeats the first piece: they end in sums that nobody takes.
+// Columns past Kc (Kc % 64 != 0) are cleared on both sides. kVec: the rows of B
+// are whole 16-byte pieces (r % 8 == 0); without it they are read value by value.
+template <int RM, int RTALL, bool kBT, int XF, bool kVec>
+__device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, const int64_t (&rows)[RM], int Kc, int qb,
+                                         int qe, const uint16_t* W, int r, u32x4* mine,
+                                         f32x4 (&acc)[RM][md_rtw<RTALL>()], int wave, int lane) {
+  constexpr int RT = md_rtw<RTALL>(), kGroups = md_groups<RTALL>(), kShares = kMdWaves / kGroups;
+  constexpr int GS = kVec ? md_gs<RM, RT>() : 1;
+  const int w = wave / kGroups, j0 = 16 * RT * (wave % kGroups);   // share of the contraction, first rank
   const int g = lane >> 4, c = lane & 15;
-  const int nchunk = (Kc + 63) / 64;
-  const bool vec = (r & 7) == 0;
-  const bool rlive = row >= 0;
-  const int64_t rs = rlive ? row : 0;
   const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int jt = 0; jt < RT; ++jt) acc[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int jt = 0; jt < RT; ++jt) acc[i][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const char* xp[RM];
+  const uint16_t* tp[RM];
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int64_t row = rows[i] < 0 ? 0 : rows[i];
+    xp[i] = static_cast<const char*>(in) + row * Kc * (XF == kActBf16 ? 2 : 1) + 16 * g * (XF == kActBf16 ? 2 : 1);
+    tp[i] = XF == kActBf16 ? nullptr : tops + row * (Kc / 64);
+  }
+  const uint16_t* wp[kBT ? 1 : RT];
+  if constexpr (!kBT) {
+#pragma unroll
+    for (int jt = 0; jt < RT; ++jt) wp[jt] = W + static_cast<int64_t>(j0 + 16 * jt + c < r ? j0 + 16 * jt + c : 0) * Kc + 16 * g;
+  }
   struct Round {
-    u32x4 xa[GS][XF == kActBf16 ? 2 : 1];
-    uint32_t top[XF == kActBf16 ? 1 : GS];
+    u32x4 x[GS][RM][XF == kActBf16 ? 2 : 1];
+    uint32_t top[XF == kActBf16 ? 1 : GS][RM];
     u32x4 wv[GS][2 * RT];
   };
   auto load_round = [&](int q0, Round& R) {
 #pragma unroll
     for (int u = 0; u < GS; ++u) {
-      const int qq = q0 + kMdWaves * u;
-      const int q = qq < nchunk ? qq : 0;
-      const int k = q * 64 + 16 * g;
-      const int k0 = k < Kc ? k : 0, k1 = k + 8 < Kc ? k + 8 : 0;
-      if constexpr (XF == kActBf16) {
-        const uint16_t* xr = static_cast<const uint16_t*>(in) + rs * Kc;
-        R.xa[u][0] = ld16(xr + k0);
-        R.xa[u][1] = ld16(xr + k1);
-      } else {
-        R.xa[u][0] = ld16(static_cast<const uint8_t*>(in) + rs * Kc + k0);
-        R.top[u] = tops[rs * (Kc / 64) + q];
+      const int qq = q0 + kShares * u;
+      // past the end every lane reads the first bytes of its operand instead (one
+      // line a load): a branch around the loads would make the waits before
+      // the other round's MFMAs drain them all
+      const bool dead = qq >= qe;
+      const int q = __builtin_amdgcn_readfirstlane(dead ? qb : qq);
+      // pieces past Kc read the row's first ones
+      const int o0 = q * 64 + 16 * g < Kc ? q * 64 : -16 * g, o1 = q * 64 + 16 * g + 8 < Kc ? q * 64 + 8 : -16 * g;
+#pragma unroll
+      for (int i = 0; i < RM; ++i) {
+        if constexpr (XF == kActBf16) {
+          R.x[u][i][0] = ld16(dead ? in : xp[i] + 2 * o0);
+          R.x[u][i][1] = ld16(dead ? in : xp[i] + 2 * o1);
+        } else {
+          R.x[u][i][0] = ld16(dead ? in : xp[i] + q * 64);
+          R.top[u][i] = *(dead ? tops : tp[i] + q);
+        }
       }
       if constexpr (kBT) {
 #pragma unroll
         for (int e = 0; e < 2 * RT; ++e) {
-          const int pc = lane + 64 * e, Rw = (pc >> 1) / RT, col = 16 * ((pc >> 1) % RT) + 8 * (pc & 1);
-          const int n = q * 64 + Rw;
+          const int pc = lane + 64 * e, n = q * 64 + (pc >> 1) / RT, col = j0 + 16 * ((pc >> 1) % RT) + 8 * (pc & 1);
           const uint16_t* wr = W + static_cast<int64_t>(n < Kc ? n : 0) * r;
-          if (vec) R.wv[u][e] = ld16(wr + (col < r ? col : 0));   // cleared when it is staged
+          if constexpr (kVec) R.wv[u][e] = ld16(dead ? W : wr + (col < r ? col : 0));
           else R.wv[u][e] = load_row8(wr, col, r, false);
         }
       } else {
 #pragma unroll
         for (int jt = 0; jt < RT; ++jt) {
-          const uint16_t* wr = W + static_cast<int64_t>(16 * jt + c < r ? 16 * jt + c : 0) * Kc;
-          R.wv[u][2 * jt] = ld16(wr + k0);
-          R.wv[u][2 * jt + 1] = ld16(wr + k1);
+          R.wv[u][2 * jt] = ld16(dead ? W : wp[jt] + o0);
+          R.wv[u][2 * jt + 1] = ld16(dead ? W : wp[jt] + o1);
         }
       }
     }
   };
   auto compute_round = [&](int q0, const Round& R) {
-    u32x4 wa[GS][RT][2];
     if constexpr (kBT) {
 #pragma unroll
       for (int u = 0; u < GS; ++u)
 #pragma unroll
         for (int e = 0; e < 2 * RT; ++e) {
-          const int pc = lane + 64 * e, sl = pc >> 1, Rw = sl / RT, col = 16 * (sl % RT) + 8 * (pc & 1);
-          const int q = q0 + kMdWaves * u;
-          const bool live = col < r && q < nchunk && q * 64 + Rw < Kc;
-          mine[u * 128 * RT + 2 * (sl ^ md_swz<RT>(Rw)) + (pc & 1)] = live ? R.wv[u][e] : zero;
+          const int pc = lane + 64 * e, sl = pc >> 1, Rw = sl / RT;
+          mine[u * 128 * RT + 2 * (sl ^ md_swz<RT>(Rw)) + (pc & 1)] = R.wv[u][e];
         }
+    }
 #pragma unroll
-      for (int u = 0; u < GS; ++u)
+    for (int u = 0; u < GS; ++u) {
+      const int q = q0 + kShares * u;
+      if (q >= qe) break;                      // wave-uniform
+      const bool tail = q * 64 + 64 > Kc;
+      const bool live0 = q * 64 + 16 * g < Kc, live1 = q * 64 + 16 * g + 8 < Kc;
+      u32x4 wa[RT][2];
 #pragma unroll
-        for (int jt = 0; jt < RT; ++jt) {
+      for (int jt = 0; jt < RT; ++jt) {
+        if constexpr (kBT) {
           s16x4 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int Rw = 16 * g + 4 * i + (c >> 2);
             v[i] = ds_read_tr(mine + u * 128 * RT, 16 * ((Rw * RT + jt) ^ md_swz<RT>(Rw)) + 4 * (c & 3));
           }
-          wa[u][jt][0] = __builtin_bit_cast(u32x4, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-          wa[u][jt][1] = __builtin_bit_cast(u32x4, __builtin_shufflevector(v[2], v[3], 0, 1, 2, 3, 4, 5, 6, 7));
+          wa[jt][0] = __builtin_bit_cast(u32x4, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+          wa[jt][1] = __builtin_bit_cast(u32x4, __builtin_shufflevector(v[2], v[3], 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+          wa[jt][0] = R.wv[u][2 * jt];
+          wa[jt][1] = R.wv[u][2 * jt + 1];
         }
-    } else {
+        if (tail) {
+          wa[jt][0] = live0 ? wa[jt][0] : zero;
+          wa[jt][1] = live1 ? wa[jt][1] : zero;
+        }
+      }
 #pragma unroll
-      for (int u = 0; u < GS; ++u)
+      for (int i = 0; i < RM; ++i) {
+        u32x4 x0, x1;
+        if constexpr (XF == kActBf16) {
+          x0 = R.x[u][i][0];
+          x1 = R.x[u][i][1];
+          if (tail) {
+            x0 = live0 ? x0 : zero;
+            x1 = live1 ? x1 : zero;
+          }
+        } else {
+          const float s = act8_scale<XF>(R.top[u][i]);
+          x0 = act8_decode8<XF>(u32x2{R.x[u][i][0].x, R.x[u][i][0].y}, s);
+          x1 = act8_decode8<XF>(u32x2{R.x[u][i][0].z, R.x[u][i][0].w}, s);
+        }
 #pragma unroll
         for (int jt = 0; jt < RT; ++jt) {
-          const bool live = 16 * jt + c < r;
-          wa[u][jt][0] = live ? R.wv[u][2 * jt] : zero;
-          wa[u][jt][1] = live ? R.wv[u][2 * jt + 1] : zero;
+          acc[i][jt] = mfma16(as_bf16x8(x0), as_bf16x8(wa[jt][0]), acc[i][jt]);
+          acc[i][jt] = mfma16(as_bf16x8(x1), as_bf16x8(wa[jt][1]), acc[i][jt]);
         }
-    }
-#pragma unroll
-    for (int u = 0; u < GS; ++u) {
-      const int q = q0 + kMdWaves * u;
-      const int k = q * 64 + 16 * g;
-      const bool live0 = q < nchunk && k < Kc, live1 = q < nchunk && k + 8 < Kc;
-      u32x4 x0, x1;
-      if constexpr (XF == kActBf16) {
-        x0 = R.xa[u][0];
-        x1 = R.xa[u][1];
-      } else {
-        const float s = act8_scale<XF>(R.top[u]);
-        x0 = act8_decode8<XF>(u32x2{R.xa[u][0].x, R.xa[u][0].y}, s);
-        x1 = act8_decode8<XF>(u32x2{R.xa[u][0].z, R.xa[u][0].w}, s);
-      }
-      x0 = live0 && rlive ? x0 : zero;
-      x1 = live1 && rlive ? x1 : zero;
-#pragma unroll
-      for (int jt = 0; jt < RT; ++jt) {
-        acc[jt] = mfma16(as_bf16x8(x0), as_bf16x8(live0 ? wa[u][jt][0] : zero), acc[jt]);
-        acc[jt] = mfma16(as_bf16x8(x1), as_bf16x8(live1 ? wa[u][jt][1] : zero), acc[jt]);
       }
     }
   };
-  constexpr int kStep = kMdWaves * GS;
+  constexpr int kStep = kShares * GS;
   Round R0;
-  if constexpr (RT * GS <= 4) {                // two rounds in registers where they fit
+  if constexpr (kVec) {                          // the next round's loads go out before this one's MFMAs
     Round R1;
-    load_round(w, R0);
-    for (int q0 = w; q0 < nchunk; q0 += 2 * kStep) {
+    load_round(qb + w, R0);
+    for (int q0 = qb + w; q0 < qe; q0 += 2 * kStep) {
       const int q1 = q0 + kStep;
       __builtin_amdgcn_sched_barrier(0);
       load_round(q1, R1);
@@ -190,81 +229,171 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, i
       compute_round(q1, R1);
     }
   } else {
-    for (int q0 = w; q0 < nchunk; q0 += kStep) {
+    for (int q0 = qb + w; q0 < qe; q0 += kStep) {
       load_round(q0, R0);
       compute_round(q0, R0);
     }
   }
 }
 
-// sum of the eight waves' parts of (row, rank j), in wave order
-template <int RT, int kPer>
-__device__ __forceinline__ float md_sum(const f32x4* red, int row, int j) {
-  const int l = ((row >> 2) << 4) | (j & 15);
-  float sum = 0.f;
+// Sums the parts of the shares in order and hands each value to put(row of the
+// 16 RM, rank, value); consecutive threads have consecutive rows.
+template <int RM, int RT, typename Put>
+__device__ __forceinline__ void down_sum(f32x4* red, const f32x4 (&acc)[RM][md_rtw<RT>()], int t, int w, int lane,
+                                         Put&& put) {
+  constexpr int kGroups = md_groups<RT>(), kShares = kMdWaves / kGroups;
 #pragma unroll
-  for (int ww = 0; ww < kMdWaves; ++ww) sum += red[ww * kPer + (j >> 4) * 64 + l][row & 3];
-  return sum;
+  for (int jt = 0; jt < md_rtw<RT>(); ++jt) {
+    __syncthreads();                             // the staged rows, or the sums of the rank tile before
+#pragma unroll
+    for (int i = 0; i < RM; ++i) red[(w * RM + i) * 64 + lane] = acc[i][jt];
+    __syncthreads();
+    for (int e = t; e < RM * 256 * kGroups; e += 64 * kMdWaves) {
+      const int row = e % (16 * RM), j = e / (16 * RM) % 16, grp = e / (256 * RM);
+      const int l = (((row & 15) >> 2) << 4) | j;
+      float sum = 0.f;
+#pragma unroll
+      for (int sh = 0; sh < kShares; ++sh) sum += red[((sh * kGroups + grp) * RM + (row >> 4)) * 64 + l][row & 3];
+      put(row, 16 * (md_rtw<RT>() * grp + jt) + j, sum);
+    }
+  }
+}
+
+// The partial sums of a row block: [S][16 RT][16 RM] fp32. Stores and the
+// counter are device-scope accesses (coherent across the XCDs' caches); every
+// wave waits for its own stores before the workgroup counts itself in. True in
+// the workgroup that arrives last; it takes the counter back to zero.
+__device__ __forceinline__ bool arrived_last(unsigned* cnt, unsigned count, int t, int* flag) {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (t == 0) {
+    const unsigned old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = old == count - 1;
+    if (old == count - 1) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *flag;
+}
+template <int RM, int RT, typename Put>
+__device__ __forceinline__ void sum_partials(const float* part, int S, int t, Put&& put) {
+  const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(part), 0, S * RM * RT * 256 * 4, 0x00020000);
+  for (int e = t; e < RM * RT * 256; e += 64 * kMdWaves) {
+    float v[kMdMaxSplit];
+#pragma unroll
+    for (int s = 0; s < kMdMaxSplit; ++s)        // past the S parts: out of range, zero
+      v[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                           prs, static_cast<uint32_t>((s * RM * RT * 256 + e) * 4), 0, 16));
+    float sum = v[0];
+#pragma unroll
+    for (int s = 1; s < kMdMaxSplit; ++s)
+      if (s < S) sum += v[s];
+    put(e % (16 * RM), e / (16 * RM), sum);
+  }
 }
 
 }  // namespace
+
+struct MdArgs {
+  const uint16_t* in;       // [M][Kc]
+  const uint16_t* W;        // [n][r Kc]
+  uint16_t* out;            // [M][rp]
+  float* part;              // [blocks][S][16 RT][16 RM]
+  unsigned* cnt;
+  u32x4* frags;
+  int64_t M, nfrag;
+  int Kc, r, rp, blocks, S, Y;
+};
 
 // s_a t (kBT false: in = x, W = A) or s_a u (kBT true: in = dY, W = B), rounded
 // to bf16 once, [M][rp] with the ranks past r zero; rows without an adapter are
 // not written. (One bf16 number each, as for a single adapter: the output is
 // bf16 itself. The scale goes in before the rounding, so that the GEMMs need
-// no scale.) A block of 16 rows takes one pass per adapter among its rows (rows
-// of a request follow each other, so mostly one); blockIdx.y deals the passes
-// out. Workgroups past `blocks` copy x into MFMA order: fragment (tile, ss, j)
-// has, at lane (g, c), columns 256 ss + 64 g + 8 j + (0 2 | 4 6 | 1 3 | 5 7)
-// of row 16 tile + c, zero past M and Kc.
-template <int RT, int GS, bool kBT>
-__global__ __launch_bounds__(64 * kMdWaves) void k_mdown(const uint16_t* in, int64_t M, int Kc, const uint16_t* W,
-                                                         MultiLora ml, int r, int rp, uint16_t* __restrict__ out,
-                                                         unsigned blocks, u32x4* __restrict__ frags, int64_t nfrag) {
-  if (blockIdx.x >= blocks) {
-    if (kBT || blockIdx.y) return;
-    const int nss = (Kc + 255) / 256;
-    const int64_t f = static_cast<int64_t>(blockIdx.x - blocks) * kMdWaves + (threadIdx.x >> 6);
-    if (f >= nfrag) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t tile = f / (8 * nss);
-    const int rest = static_cast<int>(f - tile * 8 * nss);
-    const int64_t m = 16 * tile + (lane & 15);
-    const int k = 256 * (rest >> 3) + 64 * (lane >> 4) + 8 * (rest & 7);
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (m < M && k < Kc) v = perm8(ld16(in + m * Kc + k));
-    frags[f * 64 + lane] = v;
-    return;
-  }
-  constexpr int kPer = md_per<RT, GS, kBT>();
-  __shared__ u32x4 lds[kMdWaves * kPer];
+// no scale.) A workgroup has 16 RM rows, one of S ranges of the contraction and
+// every Y-th of the adapters among its rows, one pass each (rows of a request
+// follow each other, so mostly one pass); with S or Y above 1 the passes leave
+// partial sums and the last workgroup of the row block adds them in order.
+// Workgroups past those copy x into MFMA order: fragment (tile, ss, j) has, at
+// lane (g, c), columns 256 ss + 64 g + 8 j + (0 2 | 4 6 | 1 3 | 5 7) of row 16
+// tile + c, zero past M and Kc.
+template <int RM, int RT, bool kBT>
+__global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml) {
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int c = lane & 15;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  int id = m0 + c < M ? ml.index[m0 + c] : -1;
-  if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
-  uint32_t pend = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
-  f32x4* const red = reinterpret_cast<f32x4*>(lds);
-  for (unsigned ord = 0; pend; ++ord) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(pend));
-    const uint32_t rows = static_cast<uint32_t>(__ballot(id == a)) & 0xFFFFu;
-    pend &= ~rows;
-    if (ord % gridDim.y != blockIdx.y) continue;
-    f32x4 acc[RT];
-    down_acc<RT, GS, kBT, kActBf16>(in, nullptr, (rows >> c) & 1 ? m0 + c : -1, Kc,
-                                    W + static_cast<int64_t>(a) * r * Kc, r, lds + w * kPer, acc, w, lane);
-#pragma unroll
-    for (int jt = 0; jt < RT; ++jt) red[w * kPer + jt * 64 + lane] = acc[jt];
-    const float scale = ml.scale[a];
-    __syncthreads();
-    for (int e = t; e < 16 * rp; e += 64 * kMdWaves) {
-      const int row = e / rp, j = e - row * rp;
-      if (!((rows >> row) & 1)) continue;
-      out[(m0 + row) * rp + j] = j < 16 * RT ? bf16_bits(scale * md_sum<RT, kPer>(red, row, j)) : uint16_t{0};
+  const int Kc = P.Kc, r = P.r, rp = P.rp;
+  const int wgs = P.blocks * P.S * P.Y;
+  if (static_cast<int>(blockIdx.x) >= wgs) {
+    if constexpr (!kBT) {
+      const int nss = (Kc + 255) / 256;
+      const int64_t f = static_cast<int64_t>(blockIdx.x - wgs) * kMdWaves + w;
+      if (f >= P.nfrag) return;
+      const int64_t tile = f / (8 * nss);
+      const int rest = static_cast<int>(f - tile * 8 * nss);
+      const int64_t m = 16 * tile + c;
+      const int k = 256 * (rest >> 3) + 64 * (lane >> 4) + 8 * (rest & 7);
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (m < P.M && k < Kc) v = perm8(ld16(P.in + m * Kc + k));
+      P.frags[f * 64 + lane] = v;
     }
+    return;
+  }
+  __shared__ u32x4 lds[md_lds<RM, RT, kBT>()];
+  __shared__ int flag;
+  const int block = blockIdx.x / (P.S * P.Y), s = (blockIdx.x / P.Y) % P.S, y = blockIdx.x % P.Y;
+  const int nchunk = (Kc + 63) / 64;
+  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / P.S);
+  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / P.S);
+  const int64_t m0 = static_cast<int64_t>(block) * 16 * RM;
+  // the rows' adapters: row lane of the block (RM == 1: lanes 0 .. 15)
+  int id = lane < 16 * RM && m0 + lane < P.M ? ml.index[m0 + lane] : -1;
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
+  const uint64_t any = __ballot(id >= 0);
+  if (!any) return;                              // the whole row block: nobody counts
+  uint64_t pend = any;
+  const bool direct = P.S == 1 && P.Y == 1;
+  float* const part = P.part + static_cast<int64_t>(block) * P.S * (RM * RT * 256);
+  f32x4* const red = reinterpret_cast<f32x4*>(lds);
+  constexpr int kPerWave = md_lds<RM, RT, kBT>() / kMdWaves;
+  for (int ord = 0; pend; ++ord) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(pend));
+    const uint64_t mine = __ballot(id == a);
+    pend &= ~mine;
+    if (ord % P.Y != y) continue;
+    int64_t rows[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) rows[i] = (mine >> (16 * i + c)) & 1 ? m0 + 16 * i + c : -1;
+    f32x4 acc[RM][md_rtw<RT>()];
+    const uint16_t* Wa = P.W + static_cast<int64_t>(a) * r * Kc;
+    if (!kBT || (r & 7) == 0)
+      down_acc<RM, RT, kBT, kActBf16, true>(P.in, nullptr, rows, Kc, qb, qe, Wa, r, lds + w * kPerWave, acc, w, lane);
+    else
+      down_acc<RM, RT, kBT, kActBf16, false>(P.in, nullptr, rows, Kc, qb, qe, Wa, r, lds + w * kPerWave, acc, w, lane);
+    const float scale = ml.scale[a];
+    down_sum<RM, RT>(red, acc, t, w, lane, [&](int row, int j, float v) {
+      if (!((mine >> row) & 1) || j >= rp) return;
+      if (direct)
+        P.out[(m0 + row) * rp + j] = j < r ? bf16_bits(scale * v) : uint16_t{0};
+      else
+        __hip_atomic_store(part + (s * 16 * RT + j) * 16 * RM + row, scale * v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    });
+    if (direct && 16 * RT < rp)                  // r <= 16: t has 32 columns
+      for (int e = t; e < 16 * RM * (rp - 16 * RT); e += 64 * kMdWaves) {
+        const int row = e / (rp - 16 * RT), j = 16 * RT + e % (rp - 16 * RT);
+        if ((mine >> row) & 1) P.out[(m0 + row) * rp + j] = 0;
+      }
     __syncthreads();
+  }
+  if (direct) return;
+  if (!arrived_last(P.cnt + block, P.S * P.Y, t, &flag)) return;
+  sum_partials<RM, RT>(part, P.S, t, [&](int row, int j, float v) {
+    if (!((any >> row) & 1) || j >= rp) return;
+    P.out[(m0 + row) * rp + j] = j < r ? bf16_bits(v) : uint16_t{0};
+  });
+  for (int e = t; e < 16 * RM * (rp - 16 * RT); e += 64 * kMdWaves) {
+    const int row = e / (rp - 16 * RT), j = 16 * RT + e % (rp - 16 * RT);
+    if ((any >> row) & 1) P.out[(m0 + row) * rp + j] = 0;
   }
 }
 
@@ -348,53 +477,82 @@ __device__ __forceinline__ int64_t grad_row(const GradLists& L, int64_t p, int64
   return p < M ? p : -1;
 }
 
-template <int RT, int kPer>
-__device__ __forceinline__ void store_split(const f32x4* red, uint16_t* qt, int64_t Mp, int64_t p0, int t) {
-  // 16 rows x 16 RT ranks; consecutive threads take consecutive rows of a rank
-  for (int e = t; e < 16 * 16 * RT; e += 64 * kMdWaves) {
-    const int row = e & 15, j = e >> 4;
-    float v = md_sum<RT, kPer>(red, row, j);
+// one value of t or u as three bf16 numbers, the rounded value and what is left
+// of it twice: [3][16 RT][Mp]
+template <int RT>
+__device__ __forceinline__ void put_split(uint16_t* qt, int64_t Mp, int64_t p, int j, float v) {
 #pragma unroll
-    for (int p = 0; p < kSplit; ++p) {
-      const uint16_t b = bf16_bits(v);
-      qt[(static_cast<int64_t>(p) * 16 * RT + j) * Mp + p0 + row] = b;
-      v -= bf16_lo(b);
-    }
+  for (int k = 0; k < kSplit; ++k) {
+    const uint16_t b = bf16_bits(v);
+    qt[(static_cast<int64_t>(k) * 16 * RT + j) * Mp + p] = b;
+    v -= bf16_lo(b);
   }
 }
 
-// t^T (even blocks) and u^T (odd blocks) of 16 listed rows: [3][16 RT][Mp] bf16
-template <int RT, int GS, int XF>
-__global__ __launch_bounds__(64 * kMdWaves) void k_gdown(const void* x, const uint16_t* tops, const uint16_t* dy, int64_t M,
-                                                         int N, int K, const uint16_t* A, const uint16_t* B, int r,
-                                                         GradLists L, int64_t Mp, uint16_t* __restrict__ tt,
-                                                         uint16_t* __restrict__ ut) {
-  constexpr int kPerT = md_per<RT, GS, false>(), kPerU = md_per<RT, GS, true>();
-  __shared__ u32x4 lds[kMdWaves * (kPerT > kPerU ? kPerT : kPerU)];
+struct GdArgs {
+  const void* x;            // [M][K], or its checkpoint's codes
+  const uint16_t* tops;
+  const uint16_t* dy;       // [M][N]
+  const uint16_t* A;        // [n][r][K]
+  const uint16_t* B;        // [n][N][r]
+  uint16_t *tt, *ut;        // [3][16 RT][Mp]
+  float* part;              // [chunk][t, u][S][16 RT][64]
+  unsigned* cnt;            // [chunk][t, u]
+  int64_t M, Mp;
+  int N, K, r, S;
+};
+
+// t^T (even workgroups) and u^T (odd) of the 64 listed rows of a chunk, over one
+// of S ranges of the contraction
+template <int RT, int XF>
+__global__ __launch_bounds__(64 * kMdWaves) void k_gdown(GdArgs P, GradLists L) {
+  constexpr int kLds = md_lds<4, RT, true>() > md_lds<4, RT, false>() ? md_lds<4, RT, true>() : md_lds<4, RT, false>();
+  __shared__ u32x4 lds[kLds];
+  __shared__ int flag;
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x >> 1) * 16;
+  const bool is_u = blockIdx.x & 1;
+  const int s = (blockIdx.x >> 1) % P.S, chunk = (blockIdx.x >> 1) / P.S;
   int64_t a = 0;
   if (L.rows) {
-    if ((p0 >> 6) >= L.total[0]) return;
-    a = L.chunk_adapter[p0 >> 6];
+    if (chunk >= L.total[0]) return;
+    a = L.chunk_adapter[chunk];
   }
-  const int64_t row = grad_row(L, p0 + (lane & 15), M);
-  f32x4 acc[RT];
+  const int64_t p0 = static_cast<int64_t>(chunk) * 64;
+  int64_t rows[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rows[i] = grad_row(L, p0 + 16 * i + (lane & 15), P.M);
+  // bit of each place of the chunk that holds a row
+  const int64_t own = grad_row(L, p0 + lane, P.M);
+  const uint64_t live = __ballot(own >= 0);
+  const int Kc = is_u ? P.N : P.K, nchunk = (Kc + 63) / 64;
+  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / P.S);
+  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / P.S);
+  f32x4 acc[4][md_rtw<RT>()];
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
-  if (blockIdx.x & 1) {
-    down_acc<RT, GS, true, kActBf16>(dy, nullptr, row, N, B + a * N * r, r, lds + w * kPerU, acc, w, lane);
-#pragma unroll
-    for (int jt = 0; jt < RT; ++jt) red[w * kPerU + jt * 64 + lane] = acc[jt];
-    __syncthreads();
-    store_split<RT, kPerU>(red, ut, Mp, p0, t);
+  if (is_u) {
+    u32x4* const mine = lds + w * (md_lds<4, RT, true>() / kMdWaves);
+    if ((P.r & 7) == 0)
+      down_acc<4, RT, true, kActBf16, true>(P.dy, nullptr, rows, P.N, qb, qe, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
+    else
+      down_acc<4, RT, true, kActBf16, false>(P.dy, nullptr, rows, P.N, qb, qe, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
   } else {
-    down_acc<RT, GS, false, XF>(x, tops, row, K, A + a * r * K, r, lds + w * kPerT, acc, w, lane);
-#pragma unroll
-    for (int jt = 0; jt < RT; ++jt) red[w * kPerT + jt * 64 + lane] = acc[jt];
-    __syncthreads();
-    store_split<RT, kPerT>(red, tt, Mp, p0, t);
+    down_acc<4, RT, false, XF, true>(P.x, P.tops, rows, P.K, qb, qe, P.A + a * P.r * P.K, P.r, lds, acc, w, lane);
   }
+  uint16_t* const out = is_u ? P.ut : P.tt;
+  // places without a row hold zeros
+  auto put = [&](int row, int j, float v) { put_split<RT>(out, P.Mp, p0 + row, j, (live >> row) & 1 ? v : 0.f); };
+  if (P.S == 1) {
+    down_sum<4, RT>(red, acc, t, w, lane, put);
+    return;
+  }
+  const int slot = 2 * chunk + (is_u ? 1 : 0);
+  float* const part = P.part + static_cast<int64_t>(slot) * P.S * (4 * RT * 256);
+  down_sum<4, RT>(red, acc, t, w, lane, [&](int row, int j, float v) {
+    __hip_atomic_store(part + (s * 16 * RT + j) * 64 + row, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  });
+  if (!arrived_last(P.cnt + slot, P.S, t, &flag)) return;
+  sum_partials<4, RT>(part, P.S, t, put);
 }
 
 namespace {
@@ -603,37 +761,61 @@ __global__ __launch_bounds__(256) void k_mfinish(GradLists L, int items, const f
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Row blocks of 64 (an adapter's operands are then read once for 64 rows) where
+// there are enough of them, else of 16; the contraction is split, and the
+// adapters of a row block dealt out, while that leaves at most one workgroup
+// per CU.
+MultiDownPlan multi_down_plan(int64_t M, int64_t Kc, int r, int n) {
+  MultiDownPlan p;
+  p.RM = M >= 1024 ? 4 : 1;
+  p.blocks = cdiv(M, 16 * p.RM);
+  const int64_t nchunk = cdiv(Kc, 64);
+  int64_t y = p.RM == 1 ? 256 / p.blocks : 1;
+  y = std::min<int64_t>(std::min<int64_t>(y, 16), std::min<int64_t>(n, M));
+  p.Y = std::max<int64_t>(y, 1);
+  int64_t s = 256 / (p.blocks * p.Y);
+  s = std::min(s, cdiv(nchunk, p.RM == 1 ? 4 * kMdWaves : kMdWaves));   // a round of chunks per wave
+  p.S = std::max<int64_t>(std::min<int64_t>(s, kMdMaxSplit), 1);
+  if (p.S > 1 || p.Y > 1) p.part_bytes = align256(static_cast<size_t>(p.blocks * p.S * p.RM * down_nt(r)) * 1024);
+  return p;
+}
+
 hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t Kc, const uint16_t* W,
-                             const MultiLora& ml, int r, uint16_t* out, hipStream_t stream, u32x4* frags,
-                             int64_t mtiles) {
-  const int rp = static_cast<int>(rank_pad(r));
-  const int64_t blocks = cdiv(M, 16);
-  // the passes of a block side by side where that leaves at most one workgroup per CU
-  int64_t y = 256 / blocks;
-  if (y > ml.n) y = ml.n;
-  if (y > M) y = M;
-  if (y > 16) y = 16;
-  if (y < 1) y = 1;
-  const int64_t nfrag = frags ? mtiles * cdiv(Kc, 256) * 8 : 0;
-  const dim3 grid(static_cast<unsigned>(blocks + cdiv(nfrag, kMdWaves)), static_cast<unsigned>(y)), block(64 * kMdWaves);
-  const int kc = static_cast<int>(Kc);
-  const unsigned nb = static_cast<unsigned>(blocks);
-#define QNF4_MD1(RTV, GSV, BT)                                                                                         \
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RTV, GSV, BT>), grid, block, 0, stream, in, M, kc, W, ml, r, rp, out, nb, \
-                     frags, nfrag)
-#define QNF4_MD(RTV, GSV)                 \
-  do {                                    \
-    if (wrow) QNF4_MD1(RTV, GSV, false);  \
-    else QNF4_MD1(RTV, GSV, true);        \
+                             const MultiLora& ml, int r, uint16_t* out, void* ws, float* part, hipStream_t stream,
+                             u32x4* frags, int64_t mtiles) {
+  const MultiDownPlan p = multi_down_plan(M, Kc, r, ml.n);
+  MdArgs a{};
+  a.in = in;
+  a.W = W;
+  a.out = out;
+  a.part = part;
+  a.cnt = static_cast<unsigned*>(ws);
+  a.frags = frags;
+  a.M = M;
+  a.nfrag = frags ? mtiles * cdiv(Kc, 256) * 8 : 0;
+  a.Kc = static_cast<int>(Kc);
+  a.r = r;
+  a.rp = static_cast<int>(rank_pad(r));
+  a.blocks = static_cast<int>(p.blocks);
+  a.S = static_cast<int>(p.S);
+  a.Y = static_cast<int>(p.Y);
+  const dim3 grid(static_cast<unsigned>(p.blocks * p.S * p.Y + cdiv(a.nfrag, kMdWaves))), block(64 * kMdWaves);
+#define QNF4_MD2(RMV, RTV, BT) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RMV, RTV, BT>), grid, block, 0, stream, a, ml)
+#define QNF4_MD(RTV)                                 \
+  do {                                               \
+    if (wrow && p.RM == 1) QNF4_MD2(1, RTV, false);  \
+    else if (wrow) QNF4_MD2(4, RTV, false);          \
+    else if (p.RM == 1) QNF4_MD2(1, RTV, true);      \
+    else QNF4_MD2(4, RTV, true);                     \
   } while (0)
   switch (down_nt(r)) {
-    case 1: QNF4_MD(1, 4); break;
-    case 2: QNF4_MD(2, 2); break;
-    case 4: QNF4_MD(4, 1); break;
-    default: QNF4_MD(8, 1); break;
+    case 1: QNF4_MD(1); break;
+    case 2: QNF4_MD(2); break;
+    case 4: QNF4_MD(4); break;
+    default: QNF4_MD(8); break;
   }
 #undef QNF4_MD
-#undef QNF4_MD1
+#undef QNF4_MD2
   return hipGetLastError();
 }
 
@@ -667,6 +849,11 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   const size_t q = static_cast<size_t>(kSplit) * 16 * g.nt * g.Mp * 2;
   g.tt_off = take(q);
   g.ut_off = take(q);
+  // splits of t and u: about one workgroup per CU, a round of chunks per wave
+  int64_t ds = 256 / (2 * g.chunks);
+  ds = std::min(ds, cdiv(cdiv(std::max(N, K), 64), kMdWaves));
+  g.S = std::max<int64_t>(std::min<int64_t>(ds, kMdMaxSplit), 1);
+  g.dp_off = take(g.S > 1 ? static_cast<size_t>(2 * g.chunks * g.S * 4 * g.nt) * 1024 : 0);
   g.pa_off = take(static_cast<size_t>(g.slots) * K * r * 4);
   g.pb_off = take(static_cast<size_t>(g.slots) * N * r * 4);
   g.total = off;
@@ -695,26 +882,41 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   float* pb = reinterpret_cast<float*>(wsb + g.pb_off);
   const int ni = static_cast<int>(N), ki = static_cast<int>(K), per = static_cast<int>(g.per_item);
   const int ctb = static_cast<int>(cdiv(N, kGCols)), cta = static_cast<int>(cdiv(K, kGCols));
-  const dim3 dgrid(static_cast<unsigned>(g.chunks * 8)), dblock(64 * kMdWaves);
+  GdArgs d{};
+  d.x = x;
+  d.tops = tops;
+  d.dy = dy;
+  d.A = A;
+  d.B = B;
+  d.tt = tt;
+  d.ut = ut;
+  d.part = reinterpret_cast<float*>(wsb + g.dp_off);
+  d.cnt = reinterpret_cast<unsigned*>(wsb);
+  d.M = M;
+  d.Mp = g.Mp;
+  d.N = ni;
+  d.K = ki;
+  d.r = r;
+  d.S = static_cast<int>(g.S);
+  const dim3 dgrid(static_cast<unsigned>(g.chunks * 2 * g.S)), dblock(64 * kMdWaves);
   const dim3 ggrid(static_cast<unsigned>(ctb + cta), static_cast<unsigned>(g.items));
-#define QNF4_MG(NTV, GSV, XFV)                                                                                       \
+#define QNF4_MG(NTV, XFV)                                                                                            \
   do {                                                                                                               \
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gdown<NTV, GSV, XFV>), dgrid, dblock, 0, stream, x, tops, dy, M, ni, ki, A, B, \
-                       r, L, g.Mp, tt, ut);                                                                          \
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gdown<NTV, XFV>), dgrid, dblock, 0, stream, d, L);                          \
     hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mgrad<NTV, XFV>), ggrid, dim3(256), 0, stream, x, tops, dy, M, ni, ki, r, tt, \
                        ut, g.Mp, ctb, L, per, static_cast<int>(g.chunks), scale, alpha_r, accumulate, pa, pb, dA, dB); \
   } while (0)
-#define QNF4_MGX(NTV, GSV)                              \
-  do {                                                  \
-    if (xfmt == kActBf16) QNF4_MG(NTV, GSV, kActBf16);  \
-    else if (xfmt == kActInt8) QNF4_MG(NTV, GSV, kActInt8); \
-    else QNF4_MG(NTV, GSV, kActE4m3);                   \
+#define QNF4_MGX(NTV)                                  \
+  do {                                                 \
+    if (xfmt == kActBf16) QNF4_MG(NTV, kActBf16);      \
+    else if (xfmt == kActInt8) QNF4_MG(NTV, kActInt8); \
+    else QNF4_MG(NTV, kActE4m3);                       \
   } while (0)
   switch (g.nt) {
-    case 1: QNF4_MGX(1, 4); break;
-    case 2: QNF4_MGX(2, 2); break;
-    case 4: QNF4_MGX(4, 1); break;
-    default: QNF4_MGX(8, 1); break;
+    case 1: QNF4_MGX(1); break;
+    case 2: QNF4_MGX(2); break;
+    case 4: QNF4_MGX(4); break;
+    default: QNF4_MGX(8); break;
   }
 #undef QNF4_MGX
 #undef QNF4_MG

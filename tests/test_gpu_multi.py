@@ -166,19 +166,22 @@ SHAPES = [
 
 
 @pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(40, 37, 128, 8, 3, "runs"), (260, 301, 320, 12, 3, "mixed"),
-                                                     (5, 1, 2112, 16, 2, "mixed")])
+                                                     (5, 1, 2112, 16, 2, "mixed"), (48, 200, 4160, 16, 30, "mixed"),
+                                                     # a contraction split over workgroups: the tiled kernel, ragged and whole
+                                                     (1100, 264, 2112, 16, 6, "runs"), (1030, 520, 2048, 40, 40, "mixed")])
 def test_forward(qops, M, N, K, r, n, kind):
     c = Case(qops, M, N, K, r, n, kind, 100 + M)
     c.check_fwd(qops.lora_fwd_multi(dev(c.x), c.qw, c.pool, c.index))
 
 
-@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES)
+@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(130, 1544, 320, 24, 5, "runs"), (70, 2056, 192, 64, 33, "mixed"),
+                                                     (600, 4104, 576, 16, 3, "runs"), (3, 8200, 64, 8, 2, "mixed")])
 def test_backward(qops, M, N, K, r, n, kind):
     c = Case(qops, M, N, K, r, n, kind, 200 + M)
     c.check_bwd(qops.bwd_dx_multi(dev(c.dy), c.qw, c.pool, c.index))
 
 
-@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES)
+@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(60, 2056, 4160, 80, 3, "runs"), (1300, 1032, 2112, 16, 20, "mixed")])
 def test_gradients(qops, M, N, K, r, n, kind):
     c = Case(qops, M, N, K, r, n, kind, 300 + M)
     ws = qops.Workspace("cuda")

@@ -244,6 +244,7 @@ hipError_t launch_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M, in
 // [n]; an index outside 0 .. n - 1 means none.
 // ---------------------------------------------------------------------------
 constexpr int kMaxAdapters = 4096;
+constexpr int kFindMaxM = 8192;             // rows up to which the gradients find their chunks without a listing kernel
 struct MultiLora {
   const int* index;         // [M]
   const float* scale;       // [n]
@@ -267,6 +268,7 @@ size_t multi_ws_bytes(int op, int64_t M, int64_t N, int64_t K, int r, int n);
 struct GradItem {
   int adapter, c0, c1;      // chunks [c0, c1)
   int slot;                 // partial sums, or -1: the adapter's only item, written in place
+  int items, slot0;         // items of the adapter and the first one's slot
 };
 struct GradAdapter {
   int items, slot;          // items of the adapter, its first partial slot (items > 1)
@@ -281,8 +283,8 @@ struct GradLists {
 struct MultiGradPlan {
   int nt = 1;               // rank tiles of 16 (a power of two)
   int64_t chunks = 0, Mp = 0, per_item = 1, items = 0, slots = 0;   // chunks, items and slots at most
-  int64_t S = 1;            // splits of the products t and u
-  size_t rows_off = 0, chunk_off = 0, item_off = 0, adapter_off = 0, total_off = 0;
+  int64_t St = 1, Su = 1;   // splits of the products t and u
+  size_t rows_off = 0, chunk_off = 0, item_off = 0, adapter_off = 0, total_off = 0, cnt2_off = 0;
   size_t tt_off = 0, ut_off = 0, dp_off = 0, pa_off = 0, pb_off = 0, total = 0;
 };
 MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, bool listed);

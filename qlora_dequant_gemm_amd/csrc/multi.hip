@@ -12,15 +12,18 @@
 // k_mdown  s_a t or s_a u of a batch in its own order, for the forward and
 //          backward GEMMs: 16 or 64 rows per workgroup, one pass per adapter
 //          among them; beside it, x in MFMA order for the streaming forward.
-// The gradients first list each adapter's rows (k_msort: the rows of an adapter in
-// batch order, padded to whole 64-row chunks), so that every later product has
-// one adapter per chunk and needs no masks:
+// The gradients list each adapter's rows (the rows of an adapter in batch order,
+// padded to whole chunks of 64 places), so that every product has one adapter
+// per chunk and needs no masks:
 // k_gdown  t and u over the listed rows, transposed, as three bf16 numbers
 //          that sum to the fp32 value (hi + mid + lo: fp32 gradients want more
-//          than one bf16 rounding of t and u)
+//          than one bf16 rounding of t and u; two would leave 2e-6). Up to 8192
+//          rows each workgroup finds its chunk's rows itself; above, k_msort
+//          lists them first.
 // k_mgrad  G = P^T . Q over the rows of one item (a run of chunks of one
-//          adapter), P = dY or x gathered by row, Q = t or u
-// k_mfinish sums the items of adapters with more than one, in order; zeroes the
+//          adapter), P = dY or x gathered by row, Q = t or u. An adapter's only
+//          item writes its gradient; with more, the last item to arrive sums
+//          all of them in order. Workgroups without an item clear the
 //          gradients of adapters without rows.
 // Results do not depend on scheduling: no atomic touches a sum.
 //
@@ -400,34 +403,153 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
 // ---------------------------------------------------------------------------
 // gradients
 // ---------------------------------------------------------------------------
-// Rows of each adapter, one wave per adapter. Every workgroup counts the whole
-// batch (n counters in LDS; a wave whose rows agree adds once), then each wave
-// places its adapter's chunks, items and rows after those of the adapters
-// before it.
-__global__ __launch_bounds__(256) void k_msort(const int* __restrict__ index, int64_t M, int n, int ch_per_item,
-                                               GradLists L) {
+namespace {
+
+constexpr int kGdThreads = 64 * kMdWaves;
+constexpr int kFindPer = kFindMaxM / kGdThreads;           // rows per thread
+constexpr int kAdPer = kMaxAdapters / kGdThreads;          // adapters per thread
+
+// counts the rows of every adapter; a wave whose rows agree adds once
+__device__ __forceinline__ void count_rows(int id, int n, int lane, int* hist) {
+  const int first = __builtin_amdgcn_readfirstlane(id);
+  const uint64_t live = __ballot(true);
+  if (__ballot(id == first) == live) {
+    if (static_cast<unsigned>(first) < static_cast<unsigned>(n) && lane == __builtin_ctzll(live))
+      atomicAdd(&hist[first], __builtin_popcountll(live));
+  } else if (static_cast<unsigned>(id) < static_cast<unsigned>(n)) {
+    atomicAdd(&hist[id], 1);
+  }
+}
+
+__device__ __forceinline__ int chunks_of(int rows) { return (rows + 63) >> 6; }
+__device__ __forceinline__ int items_of(int chunks, int per) { return (chunks + per - 1) / per; }
+
+// the tables of adapter a, whose chunks, items and slots start at the given numbers
+__device__ __forceinline__ void put_adapter(const GradLists& L, int a, int rows, int per, int chunk, int item, int slot) {
+  const int ch = chunks_of(rows), it = items_of(ch, per);
+  L.adapter[a] = GradAdapter{it, slot};
+  for (int i = 0; i < it; ++i) {
+    const int c0 = i * per, c1 = c0 + per;
+    L.item[item + i] = GradItem{a, chunk + c0, chunk + (c1 < ch ? c1 : ch), it > 1 ? slot + i : -1, it, it > 1 ? slot : -1};
+  }
+}
+
+// Finds chunk `chunk` of the batch: its adapter, and the rows at its 64 places
+// in `out` (-1 where there is none). Every workgroup counts the whole batch.
+// The workgroup with `tables` also writes the lists that k_mgrad reads. Returns
+// the adapter, or -1 past the last chunk. scratch: kMaxAdapters + 64 integers.
+__device__ int find_chunk(const int* __restrict__ index, int M, int n, int per, int chunk, bool tables,
+                          const GradLists& L, int* scratch, int* out, int t) {
+  int* const hist = scratch;
+  int* const sums = scratch + kMaxAdapters;                // [3][8] sums of the waves, then the place found
+  const int lane = t & 63, w = t >> 6;
+  // wave w has rows [w share, (w + 1) share): in order, 64 at a time
+  const int share = ((M + kMdWaves - 1) / kMdWaves + 63) & ~63;
+  int id[kFindPer];
+#pragma unroll
+  for (int i = 0; i < kFindPer; ++i) {
+    const int m = w * share + 64 * i + lane;
+    id[i] = 64 * i < share && m < M ? index[m] : -1;
+  }
+  for (int i = t; i < n; i += kGdThreads) hist[i] = 0;
+  if (t < 64) out[t] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kFindPer; ++i)
+    if (64 * i < share) count_rows(id[i], n, lane, hist);
+  __syncthreads();
+  // chunks, items and slots before this thread's adapters (kAdPer in a row)
+  const int per_thread = (n + kGdThreads - 1) / kGdThreads;
+  int own[3] = {0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kAdPer; ++i) {
+    const int a = t * per_thread + i;
+    if (i < per_thread && a < n) {
+      const int ch = chunks_of(hist[a]), it = items_of(ch, per);
+      own[0] += ch;
+      own[1] += it;
+      own[2] += it > 1 ? it : 0;
+    }
+  }
+  int pre[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    pre[k] = own[k];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(pre[k], o);
+      if (lane >= o) pre[k] += v;
+    }
+    if (lane == 63) sums[8 * k + w] = pre[k];
+    pre[k] -= own[k];
+  }
+  if (t == 0) sums[24] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    for (int ww = 0; ww < w; ++ww) pre[k] += sums[8 * k + ww];
+  for (int i = 0; i < per_thread; ++i) {
+    const int a = t * per_thread + i;
+    if (a >= n) break;
+    const int ch = chunks_of(hist[a]), it = items_of(ch, per);
+    if (chunk >= pre[0] && chunk < pre[0] + ch) {
+      sums[24] = a;
+      sums[25] = chunk - pre[0];
+    }
+    if (tables) {
+      put_adapter(L, a, hist[a], per, pre[0], pre[1], pre[2]);
+      if (a == n - 1) {
+        L.total[0] = pre[0] + ch;
+        L.total[1] = pre[1] + it;
+      }
+    }
+    pre[0] += ch;
+    pre[1] += it;
+    pre[2] += it > 1 ? it : 0;
+  }
+  __syncthreads();
+  const int a = sums[24];
+  if (a < 0) return -1;
+  // the adapter's rows, in batch order: places [64 k, 64 k + 64) of them
+  const int first = 64 * sums[25];
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kFindPer; ++i) mine += 64 * i < share ? __builtin_popcountll(__ballot(id[i] == a)) : 0;
+  __syncthreads();
+  if (lane == 0) sums[w] = mine;
+  __syncthreads();
+  int pos = -first;
+  for (int ww = 0; ww < w; ++ww) pos += sums[ww];
+#pragma unroll
+  for (int i = 0; i < kFindPer; ++i) {
+    if (64 * i >= share) break;
+    const uint64_t hit = __ballot(id[i] == a);
+    const int p = pos + __builtin_popcountll(hit & ((1ull << lane) - 1));
+    if (id[i] == a && p >= 0 && p < 64) out[p] = w * share + 64 * i + lane;
+    pos += __builtin_popcountll(hit);
+  }
+  __syncthreads();
+  return a;
+}
+
+}  // namespace
+
+// The lists of a batch above kFindMaxM rows, one wave per adapter: every
+// workgroup counts the whole batch, then each wave places its adapter's
+// chunks, items and rows after those of the adapters before it.
+__global__ __launch_bounds__(256) void k_msort(const int* __restrict__ index, int64_t M, int n, int per, GradLists L) {
   __shared__ int hist[kMaxAdapters];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   for (int i = t; i < n; i += 256) hist[i] = 0;
   __syncthreads();
-  for (int64_t m = t; m < M; m += 256) {
-    const int id = index[m];
-    const int first = __builtin_amdgcn_readfirstlane(id);
-    const uint64_t live = __ballot(true), same = __ballot(id == first);
-    if (same == live) {
-      if (static_cast<unsigned>(first) < static_cast<unsigned>(n) && lane == __builtin_ctzll(live))
-        atomicAdd(&hist[first], __builtin_popcountll(live));
-    } else if (static_cast<unsigned>(id) < static_cast<unsigned>(n)) {
-      atomicAdd(&hist[id], 1);
-    }
-  }
+  for (int64_t m = t; m < M; m += 256) count_rows(index[m], n, lane, hist);
   __syncthreads();
   const int a = blockIdx.x * 4 + w;
   if (a >= n) return;
   int chunks = 0, items = 0, slots = 0;
   for (int b = lane; b < a; b += 64) {
-    const int ch = (hist[b] + 63) >> 6, it = (ch + ch_per_item - 1) / ch_per_item;
+    const int ch = chunks_of(hist[b]), it = items_of(ch, per);
     chunks += ch;
     items += it;
     slots += it > 1 ? it : 0;
@@ -438,17 +560,13 @@ __global__ __launch_bounds__(256) void k_msort(const int* __restrict__ index, in
     items += __shfl_xor(items, o);
     slots += __shfl_xor(slots, o);
   }
-  const int nch = (hist[a] + 63) >> 6, nit = (nch + ch_per_item - 1) / ch_per_item;
+  const int nch = chunks_of(hist[a]);
   if (lane == 0) {
-    L.adapter[a] = GradAdapter{nit, slots};
+    put_adapter(L, a, hist[a], per, chunks, items, slots);
     if (a == n - 1) {
       L.total[0] = chunks + nch;
-      L.total[1] = items + nit;
+      L.total[1] = items + items_of(nch, per);
     }
-  }
-  for (int i = lane; i < nit; i += 64) {
-    const int c0 = i * ch_per_item, c1 = c0 + ch_per_item;
-    L.item[items + i] = GradItem{a, chunks + c0, chunks + (c1 < nch ? c1 : nch), nit > 1 ? slots + i : -1};
   }
   for (int i = lane; i < nch; i += 64) L.chunk_adapter[chunks + i] = a;
   // the rows, in batch order
@@ -471,7 +589,7 @@ __global__ __launch_bounds__(256) void k_msort(const int* __restrict__ index, in
   for (int i = pos + lane; i < nch * 64; i += 64) rows[i] = -1;
 }
 
-// the row listed at place p (no list: the batch itself)
+// the row at place p (no list: the batch itself)
 __device__ __forceinline__ int64_t grad_row(const GradLists& L, int64_t p, int64_t M) {
   if (L.rows) return L.rows[p];
   return p < M ? p : -1;
@@ -495,39 +613,56 @@ struct GdArgs {
   const uint16_t* dy;       // [M][N]
   const uint16_t* A;        // [n][r][K]
   const uint16_t* B;        // [n][N][r]
+  const int* index;         // [M], or null: one adapter
   uint16_t *tt, *ut;        // [3][16 RT][Mp]
-  float* part;              // [chunk][t, u][S][16 RT][64]
+  float* part;              // [chunk][t, u][8][16 RT][64]
   unsigned* cnt;            // [chunk][t, u]
+  unsigned* cnt2;           // k_mgrad's, cleared here: ncnt2
   int64_t M, Mp;
-  int N, K, r, S;
+  int N, K, r, n, per, St, Su, ncnt2;
+  int find;                 // the chunks are found here (k_msort has not run)
 };
 
-// t^T (even workgroups) and u^T (odd) of the 64 listed rows of a chunk, over one
-// of S ranges of the contraction
+// t^T (the first St workgroups of a chunk) and u^T (the other Su) of its 64
+// places, each over one range of the contraction
 template <int RT, int XF>
-__global__ __launch_bounds__(64 * kMdWaves) void k_gdown(GdArgs P, GradLists L) {
-  constexpr int kLds = md_lds<4, RT, true>() > md_lds<4, RT, false>() ? md_lds<4, RT, true>() : md_lds<4, RT, false>();
+__global__ __launch_bounds__(kGdThreads) void k_gdown(GdArgs P, GradLists L) {
+  constexpr int kLds0 = md_lds<4, RT, true>() > md_lds<4, RT, false>() ? md_lds<4, RT, true>() : md_lds<4, RT, false>();
+  constexpr int kLds = kLds0 * 4 > kMaxAdapters + 64 ? kLds0 : (kMaxAdapters + 64) / 4;
   __shared__ u32x4 lds[kLds];
   __shared__ int flag;
+  __shared__ int place[64];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const bool is_u = blockIdx.x & 1;
-  const int s = (blockIdx.x >> 1) % P.S, chunk = (blockIdx.x >> 1) / P.S;
-  int64_t a = 0;
-  if (L.rows) {
-    if (chunk >= L.total[0]) return;
-    a = L.chunk_adapter[chunk];
-  }
+  const int per_chunk = P.St + P.Su;
+  const int chunk = blockIdx.x / per_chunk, part_no = blockIdx.x - chunk * per_chunk;
+  const bool is_u = part_no >= P.St;
+  const int s = is_u ? part_no - P.St : part_no, S = is_u ? P.Su : P.St;
+  if (blockIdx.x == 0)
+    for (int i = t; i < P.ncnt2; i += kGdThreads) P.cnt2[i] = 0;
   const int64_t p0 = static_cast<int64_t>(chunk) * 64;
+  int64_t a = 0;
+  if (P.find) {
+    a = find_chunk(P.index, static_cast<int>(P.M), P.n, P.per, chunk, blockIdx.x == 0, L, reinterpret_cast<int*>(lds),
+                   place, t);
+    if (a < 0) return;
+    if (part_no == 0 && t < 64) L.rows[p0 + t] = place[t];
+  } else {
+    if (L.rows) {
+      if (chunk >= L.total[0]) return;
+      a = L.chunk_adapter[chunk];
+    }
+    if (t < 64) place[t] = static_cast<int>(grad_row(L, p0 + t, P.M));
+    __syncthreads();
+  }
+  a = __builtin_amdgcn_readfirstlane(static_cast<int>(a));
   int64_t rows[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) rows[i] = grad_row(L, p0 + 16 * i + (lane & 15), P.M);
-  // bit of each place of the chunk that holds a row
-  const int64_t own = grad_row(L, p0 + lane, P.M);
-  const uint64_t live = __ballot(own >= 0);
+  for (int i = 0; i < 4; ++i) rows[i] = place[16 * i + (lane & 15)];
+  const uint64_t live = __ballot(place[lane] >= 0);        // the places that hold a row
   const int Kc = is_u ? P.N : P.K, nchunk = (Kc + 63) / 64;
-  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / P.S);
-  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / P.S);
+  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / S);
+  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / S);
   f32x4 acc[4][md_rtw<RT>()];
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
   if (is_u) {
@@ -542,91 +677,118 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_gdown(GdArgs P, GradLists L) 
   uint16_t* const out = is_u ? P.ut : P.tt;
   // places without a row hold zeros
   auto put = [&](int row, int j, float v) { put_split<RT>(out, P.Mp, p0 + row, j, (live >> row) & 1 ? v : 0.f); };
-  if (P.S == 1) {
+  if (S == 1) {
     down_sum<4, RT>(red, acc, t, w, lane, put);
     return;
   }
   const int slot = 2 * chunk + (is_u ? 1 : 0);
-  float* const part = P.part + static_cast<int64_t>(slot) * P.S * (4 * RT * 256);
+  float* const part = P.part + static_cast<int64_t>(slot) * kMdMaxSplit * (4 * RT * 256);
   down_sum<4, RT>(red, acc, t, w, lane, [&](int row, int j, float v) {
     __hip_atomic_store(part + (s * 16 * RT + j) * 64 + row, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   });
-  if (!arrived_last(P.cnt + slot, P.S, t, &flag)) return;
-  sum_partials<4, RT>(part, P.S, t, put);
+  if (!arrived_last(P.cnt + slot, S, t, &flag)) return;
+  sum_partials<4, RT>(part, S, t, put);
 }
 
 namespace {
 
-constexpr int kGCols = 128;                    // columns of P per workgroup (32 per wave)
+constexpr int kGThreads = 512;
+constexpr int kGCols = 256;                    // columns of P per workgroup (32 per wave)
 
-// P tile in LDS: two halves of 64 rows x 64 columns, chunk c of row m at
+// P tile in LDS: four quarters of 64 rows x 64 columns, chunk c of row m at
 // c ^ 2 f(m), f(m) = ((m >> 3) & 3) ^ ((m >> 1) & 1), so that a transposed read
 // of 4 rows at offsets 8 G + 4 q touches each bank twice (as in grad.hip)
 __device__ __forceinline__ int g_swz(int m) { return 2 * (((m >> 3) & 3) ^ ((m >> 1) & 1)); }
 
-// One item of one 128-column tile. kTR: dA (P = x, out [r][C]); else dB
-// (P = dY, out [C][r]).
+struct MgArgs {
+  const void* x;            // [M][K], or its checkpoint's codes
+  const uint16_t* tops;
+  const uint16_t* dy;       // [M][N]
+  const uint16_t *tt, *ut;  // [3][16 NT][Mp]
+  const float* scale;       // [n], or null: alpha_r
+  float *partA, *partB;     // [slot][r][K], [slot][N][r]
+  float *dA, *dB;
+  unsigned* cnt2;           // [first slot of an adapter][column tile]
+  int64_t M, Mp;
+  float alpha_r;
+  int N, K, r, n, ctb, per, chunks, accumulate;
+};
+
+// One item of one 256-column tile. kTR: dA (P = x, out [r][C]); else dB
+// (P = dY, out [C][r]). Eight waves of 32 columns share the 64 rows of a chunk
+// and its Q; the loads of the next two chunks are in flight while one is
+// multiplied. What an adapter's items read of Q (3 x 2 bytes a rank and row) is
+// shared by 256 columns.
 template <int NT, bool kTR, int XF>
-__device__ __forceinline__ void grad_item(const void* P, const uint16_t* tops, int64_t M, int C, const uint16_t* Qt,
-                                          int64_t Mp, int r, int ct, const GradItem& it, const GradLists& L,
-                                          const float* scale, float alpha_r, int accumulate, float* part, float* out,
-                                          u32x4* tile, u32x4* qtile) {
+__device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, const GradLists& L, int ct, u32x4* tile,
+                                          u32x4* qtile) {
   constexpr int kQ = kSplit * 16 * NT * 8;     // 16-byte pieces of Q per chunk
-  constexpr int kQPer = kQ / 256 + (kQ % 256 ? 1 : 0);
+  constexpr int kQPer = (kQ + kGThreads - 1) / kGThreads;
+  constexpr int kPer = XF == kActBf16 ? 4 : 2; // 16-byte loads of P per thread and chunk
+  constexpr int kRow = XF == kActBf16 ? 32 : 16;            // lanes per row
+  const int C = kTR ? A.K : A.N, r = A.r;
+  const void* const P = kTR ? A.x : static_cast<const void*>(A.dy);
+  const uint16_t* const Qt = kTR ? A.ut : A.tt;
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int G = lane >> 4, j16 = lane & 15;
   const int c0 = ct * kGCols;
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  // this thread's pieces of a chunk: columns 8 lc .. of rows lr + 16 i
-  const int lr = t >> 4, lc = t & 15;
-  const bool cin = c0 + 8 * lc < C;
-  const int col = cin ? c0 + 8 * lc : 0;
+  // this thread's loads of a chunk: rows lr + (512 / kRow) i, from column col
+  const int lr = t / kRow, lc = t % kRow;
+  constexpr int kCols = XF == kActBf16 ? 8 : 16;
+  const int col = c0 + kCols * lc < C ? c0 + kCols * lc : 0;
   struct Regs {
-    u32x4 p[4];
-    uint32_t top[XF == kActBf16 ? 1 : 4];
+    u32x4 p[kPer];
+    uint32_t top[XF == kActBf16 ? 1 : kPer];
     u32x4 q[kQPer];
-    bool live[4];
+    uint32_t live;
   };
-  auto load = [&](int ch, const int64_t (&rows)[4], Regs& R) {
+  auto rows_of = [&](int ch, int (&rows)[kPer]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      R.live[i] = rows[i] >= 0;
-      const int64_t row = R.live[i] ? rows[i] : 0;
+    for (int i = 0; i < kPer; ++i)
+      rows[i] = static_cast<int>(grad_row(L, static_cast<int64_t>(ch) * 64 + lr + kGThreads / kRow * i, A.M));
+  };
+  auto load = [&](int ch, const int (&rows)[kPer], Regs& R) {
+    R.live = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t row = rows[i] < 0 ? 0 : rows[i];
+      R.live |= rows[i] < 0 ? 0u : 1u << i;
       if constexpr (XF == kActBf16) {
         R.p[i] = ld16(static_cast<const uint16_t*>(P) + row * C + col);
       } else {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(P) + row * C + col);
-        R.p[i].x = v.x;
-        R.p[i].y = v.y;
-        R.top[i] = tops[row * (C / 64) + (col >> 6)];
+        R.p[i] = ld16(static_cast<const uint8_t*>(P) + row * C + col);
+        R.top[i] = A.tops[row * (C / 64) + (col >> 6)];
       }
     }
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int e = t + 256 * i;
-      const int rank = e >> 3;                  // of the 3 x 16 NT
-      if (kQ % 256 == 0 || e < kQ)
-        R.q[i] = ld16(Qt + static_cast<int64_t>(rank) * Mp + static_cast<int64_t>(ch) * 64 + 8 * (e & 7));
+      const int e = t + kGThreads * i;
+      if (kQ % kGThreads == 0 || e < kQ)
+        R.q[i] = ld16(Qt + static_cast<int64_t>(e >> 3) * A.Mp + static_cast<int64_t>(ch) * 64 + 8 * (e & 7));
     }
-  };
-  auto rows_of = [&](int ch, int64_t (&rows)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rows[i] = grad_row(L, static_cast<int64_t>(ch) * 64 + lr + 16 * i, M);
   };
   auto store = [&](const Regs& R, int buf) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = lr + 16 * i;
-      u32x4 v;
-      if constexpr (XF == kActBf16) v = R.p[i];
-      else v = act8_decode8<XF>(u32x2{R.p[i].x, R.p[i].y}, act8_scale<XF>(R.top[i]));
-      tile[buf * 1024 + (lc >> 3) * 512 + m * 8 + ((lc & 7) ^ g_swz(m))] = R.live[i] ? v : zero;
+    for (int i = 0; i < kPer; ++i) {
+      const int m = lr + kGThreads / kRow * i;
+      const bool live = (R.live >> i) & 1;     // a place without a row: zeros, whatever row 0 holds
+      if constexpr (XF == kActBf16) {
+        tile[buf * 2048 + (lc >> 3) * 512 + m * 8 + ((lc & 7) ^ g_swz(m))] = live ? R.p[i] : zero;
+      } else {
+        const float s = act8_scale<XF>(R.top[i]);
+        const int q = lc >> 2, ch = 2 * (lc & 3);
+        const u32x4 v0 = act8_decode8<XF>(u32x2{R.p[i].x, R.p[i].y}, s);
+        const u32x4 v1 = act8_decode8<XF>(u32x2{R.p[i].z, R.p[i].w}, s);
+        tile[buf * 2048 + q * 512 + m * 8 + (ch ^ g_swz(m))] = live ? v0 : zero;
+        tile[buf * 2048 + q * 512 + m * 8 + ((ch + 1) ^ g_swz(m))] = live ? v1 : zero;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int e = t + 256 * i, rank = e >> 3;
-      if (kQ % 256 == 0 || e < kQ) qtile[buf * kQ + rank * 8 + ((e & 7) ^ ((rank >> 1) & 7))] = R.q[i];
+      const int e = t + kGThreads * i, rank = e >> 3;
+      if (kQ % kGThreads == 0 || e < kQ) qtile[buf * kQ + rank * 8 + ((e & 7) ^ ((rank >> 1) & 7))] = R.q[i];
     }
   };
   f32x4 acc[2][NT];
@@ -635,7 +797,7 @@ __device__ __forceinline__ void grad_item(const void* P, const uint16_t* tops, i
 #pragma unroll
     for (int jt = 0; jt < NT; ++jt) acc[b][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto compute = [&](int buf) {
-    const u32x4* T = tile + buf * 1024 + (w >> 1) * 512;
+    const u32x4* T = tile + buf * 2048 + (w >> 1) * 512;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       bf16x8 pa[2];
@@ -661,30 +823,35 @@ __device__ __forceinline__ void grad_item(const void* P, const uint16_t* tops, i
         }
     }
   };
-  // chunk ch + 1 is loaded while chunk ch is multiplied; its row numbers one chunk earlier
-  Regs R;
-  int64_t rows[4];
+  // chunk i of the item is in set i % 2; loads past the end repeat the last chunk
+  Regs R0, R1;
+  int rows[kPer];
   const int last = it.c1 - 1;
+  auto at = [&](int ch) { return ch <= last ? ch : last; };
   rows_of(it.c0, rows);
-  load(it.c0, rows, R);
-  rows_of(it.c0 + 1 <= last ? it.c0 + 1 : last, rows);
-  store(R, 0);
-  __syncthreads();
-  for (int ch = it.c0; ch < it.c1; ++ch) {
+  load(it.c0, rows, R0);
+  rows_of(at(it.c0 + 1), rows);
+  load(at(it.c0 + 1), rows, R1);
+  rows_of(at(it.c0 + 2), rows);
+  auto step = [&](int ch, Regs& R) {
     const int buf = (ch - it.c0) & 1;
-    if (ch < last) {
-      load(ch + 1, rows, R);
-      rows_of(ch + 2 <= last ? ch + 2 : last, rows);
-    }
+    store(R, buf);                             // its last readers passed the barrier of the chunk before
+    __builtin_amdgcn_sched_barrier(0);
+    load(at(ch + 2), rows, R);
+    rows_of(at(ch + 3), rows);
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier_on(tile, qtile, tile, qtile);  // this wave's LDS writes done; the loads stay in flight
     compute(buf);
-    if (ch < last) store(R, buf ^ 1);          // its last readers passed the barrier of the chunk before
-    __syncthreads();
+  };
+  for (int ch = it.c0; ch < it.c1; ch += 2) {
+    step(ch, R0);
+    if (ch + 1 < it.c1) step(ch + 1, R1);
   }
 
+  float* const out = (kTR ? A.dA : A.dB) + static_cast<int64_t>(it.adapter) * C * r;
+  const float s = A.scale ? A.scale[it.adapter] : A.alpha_r;
   const bool direct = it.slot < 0;
-  const float s = direct ? (scale ? scale[it.adapter] : alpha_r) : 1.0f;
-  float* dst = direct ? out + static_cast<int64_t>(it.adapter) * C * r : part + static_cast<int64_t>(it.slot) * C * r;
-  const bool add = direct && accumulate;
+  float* const dst = direct ? out : (kTR ? A.partA : A.partB) + static_cast<int64_t>(it.slot) * C * r;
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -695,67 +862,74 @@ __device__ __forceinline__ void grad_item(const void* P, const uint16_t* tops, i
         const int j = 16 * jt + (kTR ? 4 * G + v : j16);
         if (j < r && cc < C) {
           float* o = kTR ? dst + static_cast<int64_t>(j) * C + cc : dst + static_cast<int64_t>(cc) * r + j;
-          const float val = s * acc[b][jt][v];
-          *o = add ? *o + val : val;
+          if (direct) *o = A.accumulate ? *o + s * acc[b][jt][v] : s * acc[b][jt][v];
+          else __hip_atomic_store(o, acc[b][jt][v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       }
+  if (direct) return;
+  if (!arrived_last(A.cnt2 + static_cast<int64_t>(it.slot0) * gridDim.x + blockIdx.x, it.items, t, reinterpret_cast<int*>(tile))) return;
+  // the adapter's partials in item order, four values at a time (C % 8 == 0)
+  const int cols = C - c0 < kGCols ? C - c0 : kGCols;
+  for (int e = 4 * t; e < cols * r; e += 4 * kGThreads) {
+    const int64_t at4 = kTR ? static_cast<int64_t>(e / cols) * C + c0 + e % cols : static_cast<int64_t>(c0) * r + e;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < it.items; i0 += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = __builtin_amdgcn_readfirstlane(it.slot0 + (i0 + u < it.items ? i0 + u : i0));
+        const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
+            (kTR ? A.partA : A.partB) + static_cast<int64_t>(i) * C * r, 0, C * r * 4, 0x00020000);
+        v[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(prs, static_cast<uint32_t>(at4 * 4), 0, 16));
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u < it.items) sum += v[u];
+    }
+    f32x4* o = reinterpret_cast<f32x4*>(out + at4);
+    sum *= s;
+    *o = A.accumulate ? *o + sum : sum;
+  }
 }
 
 }  // namespace
 
 // blockIdx.x: the column tiles of dB (over dY), then those of dA (over x);
-// blockIdx.y: the item
+// blockIdx.y: the item. Past the items: the gradients of adapters without rows
+// are cleared (unless they are added to), every gridDim.y - items'th adapter.
 template <int NT, int XF>
-__global__ __launch_bounds__(256) void k_mgrad(const void* x, const uint16_t* tops, const uint16_t* dy, int64_t M, int N,
-                                               int K, int r, const uint16_t* tt, const uint16_t* ut, int64_t Mp, int ctb,
-                                               GradLists L, int ch_per_item, int chunks, const float* scale, float alpha_r,
-                                               int accumulate, float* partA, float* partB, float* dA, float* dB) {
-  __shared__ u32x4 tile[2 * 1024];
+__global__ __launch_bounds__(kGThreads) void k_mgrad(MgArgs A, GradLists L) {
+  __shared__ u32x4 tile[2 * 2048];
   __shared__ u32x4 qtile[2 * kSplit * 16 * NT * 8];
+  const bool is_b = static_cast<int>(blockIdx.x) < A.ctb;
   GradItem it;
   if (L.rows) {
-    if (static_cast<int>(blockIdx.y) >= L.total[1]) return;
+    const int items = L.total[1];
+    if (static_cast<int>(blockIdx.y) >= items) {
+      if (A.accumulate) return;
+      const int C = is_b ? A.N : A.K, c0 = (is_b ? blockIdx.x : blockIdx.x - A.ctb) * kGCols;
+      const int cols = C - c0 < kGCols ? C - c0 : kGCols;
+      for (int a = blockIdx.y - items; a < A.n; a += gridDim.y - items) {
+        if (L.adapter[a].items) continue;
+        float* const o = (is_b ? A.dB : A.dA) + static_cast<int64_t>(a) * C * A.r;
+        for (int e = 4 * threadIdx.x; e < cols * A.r; e += 4 * kGThreads)
+          *reinterpret_cast<f32x4*>(o + (is_b ? static_cast<int64_t>(c0) * A.r + e
+                                              : static_cast<int64_t>(e / cols) * C + c0 + e % cols)) =
+              f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      return;
+    }
     it = L.item[blockIdx.y];
   } else {
-    const int c0 = blockIdx.y * ch_per_item, c1 = c0 + ch_per_item;
-    it = GradItem{0, c0, c1 < chunks ? c1 : chunks, gridDim.y > 1 ? static_cast<int>(blockIdx.y) : -1};
+    const int c0 = blockIdx.y * A.per, c1 = c0 + A.per;
+    const bool one = gridDim.y == 1;
+    it = GradItem{0, c0, c1 < A.chunks ? c1 : A.chunks, one ? -1 : static_cast<int>(blockIdx.y),
+                  static_cast<int>(gridDim.y), one ? -1 : 0};
   }
-  if (static_cast<int>(blockIdx.x) < ctb)
-    grad_item<NT, false, kActBf16>(dy, nullptr, M, N, tt, Mp, r, blockIdx.x, it, L, scale, alpha_r, accumulate, partB, dB,
-                                   tile, qtile);
+  if (is_b)
+    grad_item<NT, false, kActBf16>(A, it, L, blockIdx.x, tile, qtile);
   else
-    grad_item<NT, true, XF>(x, tops, M, K, ut, Mp, r, blockIdx.x - ctb, it, L, scale, alpha_r, accumulate, partA, dA, tile,
-                            qtile);
-}
-
-// out[a] (+)= s_a * sum of the adapter's partials, in item order; adapters
-// without rows: zero (nothing when accumulating); those of one item are done.
-// nb and na are multiples of 4.
-__global__ __launch_bounds__(256) void k_mfinish(GradLists L, int items, const float* __restrict__ scale, float alpha_r,
-                                                 int accumulate, int64_t nb, const float* __restrict__ partB,
-                                                 float* __restrict__ dB, int64_t na, const float* __restrict__ partA,
-                                                 float* __restrict__ dA) {
-  const int64_t a = blockIdx.y;
-  const GradAdapter ad = L.rows ? L.adapter[a] : GradAdapter{items, 0};
-  if (ad.items == 1 || (ad.items == 0 && accumulate)) return;
-  int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  const float* p = partB;
-  float* o = dB;
-  int64_t n = nb;
-  if (i >= nb) {
-    i -= nb;
-    p = partA, o = dA, n = na;
-    if (i >= na) return;
-  }
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  if (ad.items) {
-    p += static_cast<int64_t>(ad.slot) * n + i;
-    for (int s = 0; s < ad.items; ++s) sum += *reinterpret_cast<const f32x4*>(p + s * n);
-    sum *= scale ? scale[a] : alpha_r;
-  }
-  f32x4* dst = reinterpret_cast<f32x4*>(o + a * n + i);
-  if (accumulate) sum += *dst;
-  *dst = sum;
+    grad_item<NT, true, XF>(A, it, L, blockIdx.x - A.ctb, tile, qtile);
 }
 
 // ---------------------------------------------------------------------------
@@ -823,13 +997,21 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   MultiGradPlan g;
   g.nt = down_nt(r);
   const int64_t full = cdiv(M, 64);
-  const int64_t used = listed ? (M < n ? M : n) : 0;       // adapters that can have rows
-  g.chunks = listed ? M / 64 + used : full;                // at most, with each adapter's last chunk partial
+  const int64_t used = listed ? std::min<int64_t>(M, n) : 0;       // adapters that can have rows
+  g.chunks = listed ? M / 64 + used : full;                        // at most, with each adapter's last chunk partial
   g.Mp = g.chunks * 64;
-  // about four workgroups per CU over all column tiles, whole chunks per item
+  // t and u: about two workgroups per CU, each chunk's split between them by
+  // their lengths, at least a 64-deep piece per wave
+  const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(512 / g.chunks, 2);
+  auto splits = [&](int64_t want, int64_t pieces) {
+    return std::max<int64_t>(std::min({want, cdiv(pieces, kMdWaves), int64_t{kMdMaxSplit}}), 1);
+  };
+  g.St = splits(std::max<int64_t>((q * nk + (nk + nn) / 2) / (nk + nn), 1), nk);
+  g.Su = splits(q - std::min(q - 1, g.St), nn);
+  // items: about two workgroups per CU over all column tiles; an item's
+  // partial sums (4 r bytes a column) stay small beside the rows it reads
   const int64_t ct = cdiv(N, kGCols) + cdiv(K, kGCols);
-  const int64_t want = cdiv(1024, ct);
-  g.per_item = cdiv(full, want);
+  g.per_item = std::max<int64_t>({cdiv(full, cdiv(512, ct)), r / 4, 2});
   g.items = listed ? full / g.per_item + used : cdiv(full, g.per_item);
   // slots: an adapter of I >= 2 items has more than (I - 1) per_item full chunks
   g.slots = listed ? 2 * (full / g.per_item) : (g.items > 1 ? g.items : 0);
@@ -846,14 +1028,11 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
     g.adapter_off = take(static_cast<size_t>(n) * sizeof(GradAdapter));
     g.total_off = take(8);
   }
-  const size_t q = static_cast<size_t>(kSplit) * 16 * g.nt * g.Mp * 2;
-  g.tt_off = take(q);
-  g.ut_off = take(q);
-  // splits of t and u: about one workgroup per CU, a round of chunks per wave
-  int64_t ds = 256 / (2 * g.chunks);
-  ds = std::min(ds, cdiv(cdiv(std::max(N, K), 64), kMdWaves));
-  g.S = std::max<int64_t>(std::min<int64_t>(ds, kMdMaxSplit), 1);
-  g.dp_off = take(g.S > 1 ? static_cast<size_t>(2 * g.chunks * g.S * 4 * g.nt) * 1024 : 0);
+  g.cnt2_off = take(static_cast<size_t>(g.slots * ct) * 4);
+  const size_t qb = static_cast<size_t>(kSplit) * 16 * g.nt * g.Mp * 2;
+  g.tt_off = take(qb);
+  g.ut_off = take(qb);
+  g.dp_off = take(g.St > 1 || g.Su > 1 ? static_cast<size_t>(2 * g.chunks * kMdMaxSplit * 4 * g.nt) * 1024 : 0);
   g.pa_off = take(static_cast<size_t>(g.slots) * K * r * 4);
   g.pb_off = take(static_cast<size_t>(g.slots) * N * r * 4);
   g.total = off;
@@ -866,6 +1045,8 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
                              hipStream_t stream) {
   const MultiGradPlan g = multi_grad_plan(M, N, K, r, n, index != nullptr);
   char* wsb = static_cast<char*>(ws);
+  const int ctb = static_cast<int>(cdiv(N, kGCols)), cta = static_cast<int>(cdiv(K, kGCols));
+  const bool find = index && M <= kFindMaxM;
   GradLists L{};
   if (index) {
     L.rows = reinterpret_cast<int*>(wsb + g.rows_off);
@@ -873,38 +1054,64 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
     L.item = reinterpret_cast<GradItem*>(wsb + g.item_off);
     L.adapter = reinterpret_cast<GradAdapter*>(wsb + g.adapter_off);
     L.total = reinterpret_cast<int*>(wsb + g.total_off);
-    hipLaunchKernelGGL(k_msort, dim3(static_cast<unsigned>(cdiv(n, 4))), dim3(256), 0, stream, index, M, n,
-                       static_cast<int>(g.per_item), L);
+    if (!find)
+      hipLaunchKernelGGL(k_msort, dim3(static_cast<unsigned>(cdiv(n, 4))), dim3(256), 0, stream, index, M, n,
+                         static_cast<int>(g.per_item), L);
   }
-  uint16_t* tt = reinterpret_cast<uint16_t*>(wsb + g.tt_off);
-  uint16_t* ut = reinterpret_cast<uint16_t*>(wsb + g.ut_off);
-  float* pa = reinterpret_cast<float*>(wsb + g.pa_off);
-  float* pb = reinterpret_cast<float*>(wsb + g.pb_off);
-  const int ni = static_cast<int>(N), ki = static_cast<int>(K), per = static_cast<int>(g.per_item);
-  const int ctb = static_cast<int>(cdiv(N, kGCols)), cta = static_cast<int>(cdiv(K, kGCols));
   GdArgs d{};
   d.x = x;
   d.tops = tops;
   d.dy = dy;
   d.A = A;
   d.B = B;
-  d.tt = tt;
-  d.ut = ut;
+  d.index = index;
+  d.tt = reinterpret_cast<uint16_t*>(wsb + g.tt_off);
+  d.ut = reinterpret_cast<uint16_t*>(wsb + g.ut_off);
   d.part = reinterpret_cast<float*>(wsb + g.dp_off);
   d.cnt = reinterpret_cast<unsigned*>(wsb);
+  d.cnt2 = reinterpret_cast<unsigned*>(wsb + g.cnt2_off);
   d.M = M;
   d.Mp = g.Mp;
-  d.N = ni;
-  d.K = ki;
+  d.N = static_cast<int>(N);
+  d.K = static_cast<int>(K);
   d.r = r;
-  d.S = static_cast<int>(g.S);
-  const dim3 dgrid(static_cast<unsigned>(g.chunks * 2 * g.S)), dblock(64 * kMdWaves);
-  const dim3 ggrid(static_cast<unsigned>(ctb + cta), static_cast<unsigned>(g.items));
-#define QNF4_MG(NTV, XFV)                                                                                            \
-  do {                                                                                                               \
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gdown<NTV, XFV>), dgrid, dblock, 0, stream, d, L);                          \
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mgrad<NTV, XFV>), ggrid, dim3(256), 0, stream, x, tops, dy, M, ni, ki, r, tt, \
-                       ut, g.Mp, ctb, L, per, static_cast<int>(g.chunks), scale, alpha_r, accumulate, pa, pb, dA, dB); \
+  d.n = n;
+  d.per = static_cast<int>(g.per_item);
+  d.St = static_cast<int>(g.St);
+  d.Su = static_cast<int>(g.Su);
+  d.ncnt2 = static_cast<int>(g.slots * (ctb + cta));
+  d.find = find;
+  MgArgs m{};
+  m.x = x;
+  m.tops = tops;
+  m.dy = dy;
+  m.tt = d.tt;
+  m.ut = d.ut;
+  m.scale = scale;
+  m.partA = reinterpret_cast<float*>(wsb + g.pa_off);
+  m.partB = reinterpret_cast<float*>(wsb + g.pb_off);
+  m.dA = dA;
+  m.dB = dB;
+  m.cnt2 = d.cnt2;
+  m.M = M;
+  m.Mp = g.Mp;
+  m.alpha_r = alpha_r;
+  m.N = d.N;
+  m.K = d.K;
+  m.r = r;
+  m.n = n;
+  m.ctb = ctb;
+  m.per = d.per;
+  m.chunks = static_cast<int>(g.chunks);
+  m.accumulate = accumulate;
+  const dim3 dgrid(static_cast<unsigned>(g.chunks * (g.St + g.Su)));
+  // a few workgroups without an item for adapters without rows
+  const int64_t clear = index && !accumulate ? std::min<int64_t>(n, 8) : 0;
+  const dim3 ggrid(static_cast<unsigned>(ctb + cta), static_cast<unsigned>(g.items + clear));
+#define QNF4_MG(NTV, XFV)                                                                                    \
+  do {                                                                                                       \
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gdown<NTV, XFV>), dgrid, dim3(kGdThreads), 0, stream, d, L);        \
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mgrad<NTV, XFV>), ggrid, dim3(kGThreads), 0, stream, m, L);         \
   } while (0)
 #define QNF4_MGX(NTV)                                  \
   do {                                                 \
@@ -920,12 +1127,6 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   }
 #undef QNF4_MGX
 #undef QNF4_MG
-  // nothing is left to sum or to clear: a single adapter of one item, or a
-  // list without slots that is added to
-  if (index ? (g.slots == 0 && accumulate) : g.slots == 0) return hipGetLastError();
-  const int64_t nb = N * r, na = K * r;
-  hipLaunchKernelGGL(k_mfinish, dim3(static_cast<unsigned>(cdiv((nb + na) / 4, 256)), static_cast<unsigned>(n)), dim3(256),
-                     0, stream, L, static_cast<int>(g.items), scale, alpha_r, accumulate, nb, pb, dB, na, pa, dA);
   return hipGetLastError();
 }
 

@@ -443,14 +443,24 @@ def _act_fmt(fmt):
     return _ACT[fmt]
 
 
+# the current stream of a device as an integer, without the Stream object
+# (2 us of a 10 us call); absent in some builds of torch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_entry = {}
+
+
 def _launch(fn, dev, *args):
     """Calls entry point `fn` on `dev`'s current stream, with `dev` current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(_lib.lib(), fn)(*args, stream)
+    call = _entry.get(fn)
+    if call is None:
+        call = _entry[fn] = getattr(_lib.lib(), fn)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = getattr(_lib.lib(), fn)(*args, stream)
+            status = call(*args, _raw_stream(index))
     if status:
         _lib.check(fn, status)
 

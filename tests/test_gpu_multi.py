@@ -126,11 +126,13 @@ class Case:
         rA, rB = multi.grads(x, self.dy, self.A, self.B, self.s, self.idx)
         ax = np.abs(x)
         ad = np.abs(f64(self.dy))
+        A, B = np.abs(f64(self.A)), np.abs(f64(self.B))
+        dA, dB = host(dA), host(dB)
         for a in range(self.n):
             rows = self.idx == a
             s, c = float(self.s[a]), int(rows.sum())
-            U = ad[rows] @ np.abs(f64(self.B)[a])
-            T = ax[rows] @ np.abs(f64(self.A)[a]).T
+            U = ad[rows] @ B[a]
+            T = ax[rows] @ A[a].T
             eA = (self.N + 2 * c + 16) * 2.0 ** -23 * s * (U.T @ ax[rows])
             eB = (self.K + 2 * c + 16) * 2.0 ** -23 * s * (ad[rows].T @ T)
             self.bounded(dA[a], rA[a] + dA0, eA + 2.0 ** -23 * abs(dA0), 2.0 ** -24)
@@ -138,7 +140,7 @@ class Case:
 
     @staticmethod
     def bounded(got, ref, e, rounding):
-        got = host(got)
+        got = got if isinstance(got, np.ndarray) else host(got)
         assert got.shape == ref.shape
         over = np.abs(got - ref) - (e + rounding * (np.abs(ref) + e))
         at = np.unravel_index(np.argmax(np.where(np.isnan(over), np.inf, over)), over.shape)
@@ -181,7 +183,10 @@ def test_backward(qops, M, N, K, r, n, kind):
     c.check_bwd(qops.bwd_dx_multi(dev(c.dy), c.qw, c.pool, c.index))
 
 
-@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(60, 2056, 4160, 80, 3, "runs"), (1300, 1032, 2112, 16, 20, "mixed")])
+@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(60, 2056, 4160, 80, 3, "runs"), (1300, 1032, 2112, 16, 20, "mixed"),
+                                                     # past the batch that lists itself; many adapters, most without rows
+                                                     (8200, 40, 64, 8, 5, "mixed"), (9001, 24, 128, 33, 3, "runs"),
+                                                     (100, 40, 64, 4, 4096, "mixed"), (8192, 8, 64, 4, 2, "runs")])
 def test_gradients(qops, M, N, K, r, n, kind):
     c = Case(qops, M, N, K, r, n, kind, 300 + M)
     ws = qops.Workspace("cuda")

@@ -274,8 +274,8 @@ struct GradAdapter {
   int items, slot;          // items of the adapter, its first partial slot (items > 1)
 };
 struct GradLists {
-  int* rows;                // [chunks * 64]; null: one adapter, every row in order
-  int* chunk_adapter;       // [chunks]
+  int* rows;                // [chunks * 64]
+  int* chunk_adapter;       // [chunks]; this and the others null: one adapter
   GradItem* item;
   GradAdapter* adapter;     // [n]
   int* total;               // chunks, items
@@ -285,7 +285,7 @@ struct MultiGradPlan {
   int64_t chunks = 0, Mp = 0, per_item = 1, items = 0, slots = 0;   // chunks, items and slots at most
   int64_t St = 1, Su = 1;   // splits of the products t and u
   size_t rows_off = 0, chunk_off = 0, item_off = 0, adapter_off = 0, total_off = 0, cnt2_off = 0;
-  size_t tt_off = 0, ut_off = 0, dp_off = 0, pa_off = 0, pb_off = 0, total = 0;
+  size_t tt_off = 0, ut_off = 0, dp_off = 0, part_off = 0, total = 0;
 };
 MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, bool listed);
 // xfmt: kActBf16 (x bf16), or the format of a checkpoint (x its codes, tops its

@@ -43,13 +43,13 @@ namespace qnf4 {
 
 namespace {
 
-constexpr int kMdWaves = 8;
+constexpr int kMdWaves = 4;
 constexpr int kSplit = 3;                      // bf16 numbers that carry one fp32 value of t or u
 
-// A wave takes at most two rank tiles of 16 (its registers), so the eight waves
-// are (8 / groups) shares of the contraction x groups of rank tiles.
+// A wave takes at most four rank tiles of 16 (its registers), so the four waves
+// are (4 / groups) shares of the contraction x groups of rank tiles.
 template <int RT>
-constexpr int md_rtw() { return RT < 2 ? RT : 2; }
+constexpr int md_rtw() { return RT < 4 ? RT : 4; }
 template <int RT>
 constexpr int md_groups() { return RT / md_rtw<RT>(); }
 
@@ -60,14 +60,15 @@ constexpr int md_groups() { return RT / md_rtw<RT>(); }
 template <int RTW>
 __device__ __forceinline__ int md_swz(int R) {
   if constexpr (RTW == 1) return ((R >> 4) & 1) << 2;
-  else return (R >> 4) & 1;
+  else if constexpr (RTW == 2) return (R >> 4) & 1;
+  else return ((R >> 1) & 1) | (((R >> 4) & 1) << 1);
 }
 
 // 64-deep chunks of a round (all their loads go out together); two rounds are
 // in registers
 template <int RM, int RTW>
 constexpr int md_gs() {
-  if constexpr (RM == 1) return RTW == 1 ? 4 : 2;
+  if constexpr (RM == 1) return RTW == 1 ? 4 : RTW == 2 ? 2 : 1;
   else return RTW == 1 ? 2 : 1;
 }
 // LDS chunks (16 bytes) of a workgroup: the waves' staged adapter rows, or
@@ -79,8 +80,7 @@ constexpr int md_lds() {
 }
 
 // This wave's share of the product of 16 RM rows of `in` with the adapter W
-// (kBT: B [Kc][r], else A [r][Kc]) over the 64-deep chunks [qb, qe): chunks qb +
-// w, qb + w + 8, ... Lane (g, c) supplies 16 elements at 16 g of each chunk of
+// (kBT: B [Kc][r], else A [r][Kc]) over the 64-deep chunks [qb, qe): its share's of them Lane (g, c) supplies 16 elements at 16 g of each chunk of
 // row rows[i] of tile i. XF: the format of `in` (kActBf16, or a checkpoint with
 // one constant per 64 values in `tops`). An absent row (< 0) repeats row 0 and a
 // rank past r repeats the first piece: they end in sums that nobody takes.
@@ -88,7 +88,7 @@ constexpr int md_lds() {
 // are whole 16-byte pieces (r % 8 == 0); without it they are read value by value.
 template <int RM, int RTALL, bool kBT, int XF, bool kVec>
 __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, const int64_t (&rows)[RM], int Kc, int qb,
-                                         int qe, const uint16_t* W, int r, u32x4* mine,
+                                         int qe, int rot, const uint16_t* W, int r, u32x4* mine,
                                          f32x4 (&acc)[RM][md_rtw<RTALL>()], int wave, int lane) {
   constexpr int RT = md_rtw<RTALL>(), kGroups = md_groups<RTALL>(), kShares = kMdWaves / kGroups;
   constexpr int GS = kVec ? md_gs<RM, RT>() : 1;
@@ -112,6 +112,12 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, c
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) wp[jt] = W + static_cast<int64_t>(j0 + 16 * jt + c < r ? j0 + 16 * jt + c : 0) * Kc + 16 * g;
   }
+  // the chunks in an order turned by `rot`: workgroups that run side by side
+  // then read different columns of their rows (whose stride is mostly a
+  // multiple of what the memory channels interleave)
+  const int span = qe - qb;
+  rot = span > 0 ? rot % span : 0;
+  auto turned = [&](int q) { return q + rot < qe ? q + rot : q + rot - span; };
   struct Round {
     u32x4 x[GS][RM][XF == kActBf16 ? 2 : 1];
     uint32_t top[XF == kActBf16 ? 1 : GS][RM];
@@ -120,12 +126,12 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, c
   auto load_round = [&](int q0, Round& R) {
 #pragma unroll
     for (int u = 0; u < GS; ++u) {
-      const int qq = q0 + kShares * u;
+      const int qq = q0 + kShares * u;         // the chunk's number before the rotation
       // past the end every lane reads the first bytes of its operand instead (one
       // line a load): a branch around the loads would make the waits before
       // the other round's MFMAs drain them all
       const bool dead = qq >= qe;
-      const int q = __builtin_amdgcn_readfirstlane(dead ? qb : qq);
+      const int q = __builtin_amdgcn_readfirstlane(dead ? qb : turned(qq));
       // pieces past Kc read the row's first ones
       const int o0 = q * 64 + 16 * g < Kc ? q * 64 : -16 * g, o1 = q * 64 + 16 * g + 8 < Kc ? q * 64 + 8 : -16 * g;
 #pragma unroll
@@ -167,8 +173,8 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, c
     }
 #pragma unroll
     for (int u = 0; u < GS; ++u) {
-      const int q = q0 + kShares * u;
-      if (q >= qe) break;                      // wave-uniform
+      if (q0 + kShares * u >= qe) break;       // wave-uniform
+      const int q = turned(q0 + kShares * u);
       const bool tail = q * 64 + 64 > Kc;
       const bool live0 = q * 64 + 16 * g < Kc, live1 = q * 64 + 16 * g + 8 < Kc;
       u32x4 wa[RT][2];
@@ -239,8 +245,10 @@ __device__ __forceinline__ void down_acc(const void* in, const uint16_t* tops, c
   }
 }
 
-// Sums the parts of the shares in order and hands each value to put(row of the
-// 16 RM, rank, value); consecutive threads have consecutive rows.
+// Sums the parts of the shares in order and hands them to put(place, row, rank,
+// four values of rows row .. row + 3); `place` numbers the groups of four within
+// the workgroup's 16 RM x 16 RT values, consecutive threads having consecutive
+// places.
 template <int RM, int RT, typename Put>
 __device__ __forceinline__ void down_sum(f32x4* red, const f32x4 (&acc)[RM][md_rtw<RT>()], int t, int w, int lane,
                                          Put&& put) {
@@ -251,21 +259,31 @@ __device__ __forceinline__ void down_sum(f32x4* red, const f32x4 (&acc)[RM][md_r
 #pragma unroll
     for (int i = 0; i < RM; ++i) red[(w * RM + i) * 64 + lane] = acc[i][jt];
     __syncthreads();
-    for (int e = t; e < RM * 256 * kGroups; e += 64 * kMdWaves) {
-      const int row = e % (16 * RM), j = e / (16 * RM) % 16, grp = e / (256 * RM);
-      const int l = (((row & 15) >> 2) << 4) | j;
-      float sum = 0.f;
+    for (int e = t; e < RM * 64 * kGroups; e += 64 * kMdWaves) {
+      const int l = e % 64, i = e / 64 % RM, grp = e / (64 * RM);
+      f32x4 sum = red[(grp * RM + i) * 64 + l];
 #pragma unroll
-      for (int sh = 0; sh < kShares; ++sh) sum += red[((sh * kGroups + grp) * RM + (row >> 4)) * 64 + l][row & 3];
-      put(row, 16 * (md_rtw<RT>() * grp + jt) + j, sum);
+      for (int sh = 1; sh < kShares; ++sh) sum += red[((sh * kGroups + grp) * RM + i) * 64 + l];
+      put(jt * (RM * 64 * kGroups) + e, 16 * i + 4 * (l >> 4), 16 * (md_rtw<RT>() * grp + jt) + (l & 15), sum);
     }
   }
 }
 
-// The partial sums of a row block: [S][16 RT][16 RM] fp32. Stores and the
-// counter are device-scope accesses (coherent across the XCDs' caches); every
-// wave waits for its own stores before the workgroup counts itself in. True in
-// the workgroup that arrives last; it takes the counter back to zero.
+// Partial sums that another workgroup adds up: 16-byte stores and loads with
+// the device-coherence bit, so that they are seen across the XCDs' caches
+// without flushing them (4-byte ones cost the kernels a third of their time).
+__device__ __forceinline__ void put_part(const __amdgpu_buffer_rsrc_t& rs, int place, const f32x4& v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, static_cast<uint32_t>(place * 16), 0, 16);
+}
+__device__ __forceinline__ f32x4 get_part(const __amdgpu_buffer_rsrc_t& rs, int place) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, static_cast<uint32_t>(place * 16), 0, 16));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t part_rsrc(float* part, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(part, 0, bytes, 0x00020000);
+}
+
+// Every wave waits for its own partial sums before the workgroup counts itself
+// in. True in the workgroup that arrives last; it takes the counter back to zero.
 __device__ __forceinline__ bool arrived_last(unsigned* cnt, unsigned count, int t, int* flag) {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0);
@@ -278,21 +296,20 @@ __device__ __forceinline__ bool arrived_last(unsigned* cnt, unsigned count, int 
   __syncthreads();
   return *flag;
 }
+// the partial sums [S][RM RT 64] of a row block, in order, handed on as by down_sum
 template <int RM, int RT, typename Put>
-__device__ __forceinline__ void sum_partials(const float* part, int S, int t, Put&& put) {
-  const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<float*>(part), 0, S * RM * RT * 256 * 4, 0x00020000);
-  for (int e = t; e < RM * RT * 256; e += 64 * kMdWaves) {
-    float v[kMdMaxSplit];
+__device__ __forceinline__ void sum_partials(const __amdgpu_buffer_rsrc_t& rs, int S, int t, Put&& put) {
+  constexpr int kGroups = md_groups<RT>(), kCount = RM * RT * 64;
+  for (int p = t; p < kCount; p += 64 * kMdWaves) {
+    f32x4 v[kMdMaxSplit];
 #pragma unroll
-    for (int s = 0; s < kMdMaxSplit; ++s)        // past the S parts: out of range, zero
-      v[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                           prs, static_cast<uint32_t>((s * RM * RT * 256 + e) * 4), 0, 16));
-    float sum = v[0];
+    for (int s = 0; s < kMdMaxSplit; ++s) v[s] = get_part(rs, s * kCount + p);   // past the S parts: out of range, zero
+    f32x4 sum = v[0];
 #pragma unroll
     for (int s = 1; s < kMdMaxSplit; ++s)
       if (s < S) sum += v[s];
-    put(e % (16 * RM), e / (16 * RM), sum);
+    const int jt = p / (RM * 64 * kGroups), e = p % (RM * 64 * kGroups), l = e % 64;
+    put(p, 16 * (e / 64 % RM) + 4 * (l >> 4), 16 * (md_rtw<RT>() * (e / (64 * RM)) + jt) + (l & 15), sum);
   }
 }
 
@@ -302,7 +319,7 @@ struct MdArgs {
   const uint16_t* in;       // [M][Kc]
   const uint16_t* W;        // [n][r Kc]
   uint16_t* out;            // [M][rp]
-  float* part;              // [blocks][S][16 RT][16 RM]
+  float* part;              // [blocks][S][16 RT x 16 RM]
   unsigned* cnt;
   u32x4* frags;
   int64_t M, nfrag;
@@ -356,7 +373,9 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
   if (!any) return;                              // the whole row block: nobody counts
   uint64_t pend = any;
   const bool direct = P.S == 1 && P.Y == 1;
-  float* const part = P.part + static_cast<int64_t>(block) * P.S * (RM * RT * 256);
+  constexpr int kCount = RM * RT * 64;           // groups of four partial sums
+  const __amdgpu_buffer_rsrc_t part =
+      part_rsrc(P.part + static_cast<int64_t>(block) * P.S * kCount * 4, P.S * kCount * 16);
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
   constexpr int kPerWave = md_lds<RM, RT, kBT>() / kMdWaves;
   for (int ord = 0; pend; ++ord) {
@@ -370,16 +389,28 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
     f32x4 acc[RM][md_rtw<RT>()];
     const uint16_t* Wa = P.W + static_cast<int64_t>(a) * r * Kc;
     if (!kBT || (r & 7) == 0)
-      down_acc<RM, RT, kBT, kActBf16, true>(P.in, nullptr, rows, Kc, qb, qe, Wa, r, lds + w * kPerWave, acc, w, lane);
+      down_acc<RM, RT, kBT, kActBf16, true>(P.in, nullptr, rows, Kc, qb, qe, 5 * block, Wa, r, lds + w * kPerWave, acc, w, lane);
     else
-      down_acc<RM, RT, kBT, kActBf16, false>(P.in, nullptr, rows, Kc, qb, qe, Wa, r, lds + w * kPerWave, acc, w, lane);
+      down_acc<RM, RT, kBT, kActBf16, false>(P.in, nullptr, rows, Kc, qb, qe, 5 * block, Wa, r, lds + w * kPerWave, acc, w, lane);
     const float scale = ml.scale[a];
-    down_sum<RM, RT>(red, acc, t, w, lane, [&](int row, int j, float v) {
-      if (!((mine >> row) & 1) || j >= rp) return;
-      if (direct)
-        P.out[(m0 + row) * rp + j] = j < r ? bf16_bits(scale * v) : uint16_t{0};
-      else
-        __hip_atomic_store(part + (s * 16 * RT + j) * 16 * RM + row, scale * v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    down_sum<RM, RT>(red, acc, t, w, lane, [&](int place, int row, int j, f32x4 v) {
+      v *= scale;
+      if (!direct) {
+        // the block's partials are written once for all its passes: rows of
+        // other adapters keep what their pass left
+        if (any == mine) put_part(part, s * kCount + place, v);
+        else
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((mine >> (row + q)) & 1)
+              __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, static_cast<float>(v[q])), part,
+                                                    static_cast<uint32_t>((s * kCount + place) * 16 + 4 * q), 0, 16);
+        return;
+      }
+      if (j >= rp) return;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((mine >> (row + q)) & 1) P.out[(m0 + row + q) * rp + j] = j < r ? bf16_bits(v[q]) : uint16_t{0};
     });
     if (direct && 16 * RT < rp)                  // r <= 16: t has 32 columns
       for (int e = t; e < 16 * RM * (rp - 16 * RT); e += 64 * kMdWaves) {
@@ -390,9 +421,11 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
   }
   if (direct) return;
   if (!arrived_last(P.cnt + block, P.S * P.Y, t, &flag)) return;
-  sum_partials<RM, RT>(part, P.S, t, [&](int row, int j, float v) {
-    if (!((any >> row) & 1) || j >= rp) return;
-    P.out[(m0 + row) * rp + j] = j < r ? bf16_bits(v) : uint16_t{0};
+  sum_partials<RM, RT>(part, P.S, t, [&](int, int row, int j, const f32x4& v) {
+    if (j >= rp) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if ((any >> (row + q)) & 1) P.out[(m0 + row + q) * rp + j] = j < r ? bf16_bits(v[q]) : uint16_t{0};
   });
   for (int e = t; e < 16 * RM * (rp - 16 * RT); e += 64 * kMdWaves) {
     const int row = e / (rp - 16 * RT), j = 16 * RT + e % (rp - 16 * RT);
@@ -589,23 +622,25 @@ __global__ __launch_bounds__(256) void k_msort(const int* __restrict__ index, in
   for (int i = pos + lane; i < nch * 64; i += 64) rows[i] = -1;
 }
 
-// the row at place p (no list: the batch itself)
-__device__ __forceinline__ int64_t grad_row(const GradLists& L, int64_t p, int64_t M) {
-  if (L.rows) return L.rows[p];
-  return p < M ? p : -1;
-}
-
-// one value of t or u as three bf16 numbers, the rounded value and what is left
-// of it twice: [3][16 RT][Mp]
+// four values of t or u (places row .. row + 3 of a chunk, rank j) as three bf16
+// numbers each, the rounded value and what is left of it twice:
+// [chunk][3][16 RT][64], a chunk in one piece (ranks at a stride of a whole row
+// length would share one memory channel)
 template <int RT>
-__device__ __forceinline__ void put_split(uint16_t* qt, int64_t Mp, int64_t p, int j, float v) {
+__device__ __forceinline__ void put_split(uint16_t* qt, int64_t chunk, int row, int j, f32x4 v) {
 #pragma unroll
   for (int k = 0; k < kSplit; ++k) {
-    const uint16_t b = bf16_bits(v);
-    qt[(static_cast<int64_t>(k) * 16 * RT + j) * Mp + p] = b;
-    v -= bf16_lo(b);
+    u32x2 b;
+    b.x = pack_bf16x2(v[0], v[1]);
+    b.y = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<u32x2*>(qt + ((chunk * kSplit + k) * 16 * RT + j) * 64 + row) = b;
+    v -= f32x4{bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)};
   }
 }
+
+// how k_gdown knows a chunk's rows: it finds them, k_msort has listed them, or
+// there is one adapter and they are the batch's own
+constexpr int kGdFind = 0, kGdListed = 1, kGdWhole = 2;
 
 struct GdArgs {
   const void* x;            // [M][K], or its checkpoint's codes
@@ -613,14 +648,14 @@ struct GdArgs {
   const uint16_t* dy;       // [M][N]
   const uint16_t* A;        // [n][r][K]
   const uint16_t* B;        // [n][N][r]
-  const int* index;         // [M], or null: one adapter
-  uint16_t *tt, *ut;        // [3][16 RT][Mp]
-  float* part;              // [chunk][t, u][8][16 RT][64]
+  const int* index;         // [M]
+  uint16_t *tt, *ut;        // [chunk][3][16 RT][64]
+  float* part;              // [chunk][t, u][kMdMaxSplit][16 RT x 64]
   unsigned* cnt;            // [chunk][t, u]
   unsigned* cnt2;           // k_mgrad's, cleared here: ncnt2
-  int64_t M, Mp;
+  int64_t M;
   int N, K, r, n, per, St, Su, ncnt2;
-  int find;                 // the chunks are found here (k_msort has not run)
+  int mode;
 };
 
 // t^T (the first St workgroups of a chunk) and u^T (the other Su) of its 64
@@ -642,19 +677,20 @@ __global__ __launch_bounds__(kGdThreads) void k_gdown(GdArgs P, GradLists L) {
     for (int i = t; i < P.ncnt2; i += kGdThreads) P.cnt2[i] = 0;
   const int64_t p0 = static_cast<int64_t>(chunk) * 64;
   int64_t a = 0;
-  if (P.find) {
+  if (P.mode == kGdFind) {
     a = find_chunk(P.index, static_cast<int>(P.M), P.n, P.per, chunk, blockIdx.x == 0, L, reinterpret_cast<int*>(lds),
                    place, t);
     if (a < 0) return;
-    if (part_no == 0 && t < 64) L.rows[p0 + t] = place[t];
+  } else if (P.mode == kGdListed) {
+    if (chunk >= L.total[0]) return;
+    a = L.chunk_adapter[chunk];
+    if (t < 64) place[t] = L.rows[p0 + t];
+    __syncthreads();
   } else {
-    if (L.rows) {
-      if (chunk >= L.total[0]) return;
-      a = L.chunk_adapter[chunk];
-    }
-    if (t < 64) place[t] = static_cast<int>(grad_row(L, p0 + t, P.M));
+    if (t < 64) place[t] = p0 + t < P.M ? static_cast<int>(p0 + t) : -1;
     __syncthreads();
   }
+  if (P.mode != kGdListed && part_no == 0 && t < 64) L.rows[p0 + t] = place[t];
   a = __builtin_amdgcn_readfirstlane(static_cast<int>(a));
   int64_t rows[4];
 #pragma unroll
@@ -668,32 +704,40 @@ __global__ __launch_bounds__(kGdThreads) void k_gdown(GdArgs P, GradLists L) {
   if (is_u) {
     u32x4* const mine = lds + w * (md_lds<4, RT, true>() / kMdWaves);
     if ((P.r & 7) == 0)
-      down_acc<4, RT, true, kActBf16, true>(P.dy, nullptr, rows, P.N, qb, qe, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
+      down_acc<4, RT, true, kActBf16, true>(P.dy, nullptr, rows, P.N, qb, qe, 5 * chunk, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
     else
-      down_acc<4, RT, true, kActBf16, false>(P.dy, nullptr, rows, P.N, qb, qe, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
+      down_acc<4, RT, true, kActBf16, false>(P.dy, nullptr, rows, P.N, qb, qe, 5 * chunk, P.B + a * P.N * P.r, P.r, mine, acc, w, lane);
   } else {
-    down_acc<4, RT, false, XF, true>(P.x, P.tops, rows, P.K, qb, qe, P.A + a * P.r * P.K, P.r, lds, acc, w, lane);
+    down_acc<4, RT, false, XF, true>(P.x, P.tops, rows, P.K, qb, qe, 5 * chunk, P.A + a * P.r * P.K, P.r, lds, acc, w, lane);
   }
   uint16_t* const out = is_u ? P.ut : P.tt;
   // places without a row hold zeros
-  auto put = [&](int row, int j, float v) { put_split<RT>(out, P.Mp, p0 + row, j, (live >> row) & 1 ? v : 0.f); };
+  auto put = [&](int, int row, int j, f32x4 v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (live >> (row + q)) & 1 ? v[q] : 0.f;
+    put_split<RT>(out, chunk, row, j, v);
+  };
   if (S == 1) {
     down_sum<4, RT>(red, acc, t, w, lane, put);
     return;
   }
+  constexpr int kCount = 4 * RT * 64;
   const int slot = 2 * chunk + (is_u ? 1 : 0);
-  float* const part = P.part + static_cast<int64_t>(slot) * kMdMaxSplit * (4 * RT * 256);
-  down_sum<4, RT>(red, acc, t, w, lane, [&](int row, int j, float v) {
-    __hip_atomic_store(part + (s * 16 * RT + j) * 64 + row, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  });
+  const __amdgpu_buffer_rsrc_t part =
+      part_rsrc(P.part + static_cast<int64_t>(slot) * kMdMaxSplit * kCount * 4, S * kCount * 16);
+  down_sum<4, RT>(red, acc, t, w, lane, [&](int place, int, int, const f32x4& v) { put_part(part, s * kCount + place, v); });
   if (!arrived_last(P.cnt + slot, S, t, &flag)) return;
   sum_partials<4, RT>(part, S, t, put);
 }
 
 namespace {
 
-constexpr int kGThreads = 512;
-constexpr int kGCols = 256;                    // columns of P per workgroup (32 per wave)
+constexpr int kGThreads = 256;
+constexpr int kGCols = 256;                    // columns of P per workgroup (64 per wave)
+
+// two LDS buffers of P and Q where one workgroup fills a CU anyway
+template <int NT>
+constexpr bool mg_two() { return NT >= 4; }
 
 // P tile in LDS: four quarters of 64 rows x 64 columns, chunk c of row m at
 // c ^ 2 f(m), f(m) = ((m >> 3) & 3) ^ ((m >> 1) & 1), so that a transposed read
@@ -704,27 +748,28 @@ struct MgArgs {
   const void* x;            // [M][K], or its checkpoint's codes
   const uint16_t* tops;
   const uint16_t* dy;       // [M][N]
-  const uint16_t *tt, *ut;  // [3][16 NT][Mp]
+  const uint16_t *tt, *ut;  // [chunk][3][16 NT][64]
   const float* scale;       // [n], or null: alpha_r
-  float *partA, *partB;     // [slot][r][K], [slot][N][r]
+  float* part;              // [slot][column tile][256 columns x 16 NT ranks]
   float *dA, *dB;
   unsigned* cnt2;           // [first slot of an adapter][column tile]
-  int64_t M, Mp;
+  int64_t M;
   float alpha_r;
   int N, K, r, n, ctb, per, chunks, accumulate;
 };
 
 // One item of one 256-column tile. kTR: dA (P = x, out [r][C]); else dB
-// (P = dY, out [C][r]). Eight waves of 32 columns share the 64 rows of a chunk
+// (P = dY, out [C][r]). Four waves of 64 columns share the 64 rows of a chunk
 // and its Q; the loads of the next two chunks are in flight while one is
-// multiplied. What an adapter's items read of Q (3 x 2 bytes a rank and row) is
-// shared by 256 columns.
+// multiplied. At high ranks the LDS reads of Q bound the kernel (three numbers
+// a value, read by every wave), so a wave multiplies each fragment with four
+// column tiles.
 template <int NT, bool kTR, int XF>
-__device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, const GradLists& L, int ct, u32x4* tile,
-                                          u32x4* qtile) {
+__device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, const GradLists& L, int ct, u32x4* tiles,
+                                          u32x4* qtiles) {
   constexpr int kQ = kSplit * 16 * NT * 8;     // 16-byte pieces of Q per chunk
   constexpr int kQPer = (kQ + kGThreads - 1) / kGThreads;
-  constexpr int kPer = XF == kActBf16 ? 4 : 2; // 16-byte loads of P per thread and chunk
+  constexpr int kPer = XF == kActBf16 ? 8 : 4; // 16-byte loads of P per thread and chunk
   constexpr int kRow = XF == kActBf16 ? 32 : 16;            // lanes per row
   const int C = kTR ? A.K : A.N, r = A.r;
   const void* const P = kTR ? A.x : static_cast<const void*>(A.dy);
@@ -734,7 +779,7 @@ __device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, c
   const int G = lane >> 4, j16 = lane & 15;
   const int c0 = ct * kGCols;
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  // this thread's loads of a chunk: rows lr + (512 / kRow) i, from column col
+  // this thread's loads of a chunk: rows lr + (256 / kRow) i, from column col
   const int lr = t / kRow, lc = t % kRow;
   constexpr int kCols = XF == kActBf16 ? 8 : 16;
   const int col = c0 + kCols * lc < C ? c0 + kCols * lc : 0;
@@ -747,7 +792,7 @@ __device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, c
   auto rows_of = [&](int ch, int (&rows)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      rows[i] = static_cast<int>(grad_row(L, static_cast<int64_t>(ch) * 64 + lr + kGThreads / kRow * i, A.M));
+      rows[i] = L.rows[static_cast<int64_t>(ch) * 64 + lr + kGThreads / kRow * i];
   };
   auto load = [&](int ch, const int (&rows)[kPer], Regs& R) {
     R.live = 0;
@@ -766,130 +811,216 @@ __device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, c
     for (int i = 0; i < kQPer; ++i) {
       const int e = t + kGThreads * i;
       if (kQ % kGThreads == 0 || e < kQ)
-        R.q[i] = ld16(Qt + static_cast<int64_t>(e >> 3) * A.Mp + static_cast<int64_t>(ch) * 64 + 8 * (e & 7));
+        R.q[i] = ld16(Qt + (static_cast<int64_t>(ch) * kQ + e) * 8);
     }
   };
+  constexpr bool kTwo = mg_two<NT>();
   auto store = [&](const Regs& R, int buf) {
+    u32x4* const tile = tiles + (kTwo ? buf * 2048 : 0);
+    u32x4* const qtile = qtiles + (kTwo ? buf * kQ : 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int m = lr + kGThreads / kRow * i;
       const bool live = (R.live >> i) & 1;     // a place without a row: zeros, whatever row 0 holds
       if constexpr (XF == kActBf16) {
-        tile[buf * 2048 + (lc >> 3) * 512 + m * 8 + ((lc & 7) ^ g_swz(m))] = live ? R.p[i] : zero;
+        tile[(lc >> 3) * 512 + m * 8 + ((lc & 7) ^ g_swz(m))] = live ? R.p[i] : zero;
       } else {
         const float s = act8_scale<XF>(R.top[i]);
         const int q = lc >> 2, ch = 2 * (lc & 3);
         const u32x4 v0 = act8_decode8<XF>(u32x2{R.p[i].x, R.p[i].y}, s);
         const u32x4 v1 = act8_decode8<XF>(u32x2{R.p[i].z, R.p[i].w}, s);
-        tile[buf * 2048 + q * 512 + m * 8 + (ch ^ g_swz(m))] = live ? v0 : zero;
-        tile[buf * 2048 + q * 512 + m * 8 + ((ch + 1) ^ g_swz(m))] = live ? v1 : zero;
+        tile[q * 512 + m * 8 + (ch ^ g_swz(m))] = live ? v0 : zero;
+        tile[q * 512 + m * 8 + ((ch + 1) ^ g_swz(m))] = live ? v1 : zero;
       }
     }
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
       const int e = t + kGThreads * i, rank = e >> 3;
-      if (kQ % kGThreads == 0 || e < kQ) qtile[buf * kQ + rank * 8 + ((e & 7) ^ ((rank >> 1) & 7))] = R.q[i];
+      if (kQ % kGThreads == 0 || e < kQ) qtile[rank * 8 + ((e & 7) ^ ((rank >> 1) & 7))] = R.q[i];
     }
   };
-  f32x4 acc[2][NT];
+  f32x4 acc[4][NT];
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < 4; ++b)
 #pragma unroll
     for (int jt = 0; jt < NT; ++jt) acc[b][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](int buf) {
-    const u32x4* T = tile + buf * 2048 + (w >> 1) * 512;
+  // operands of a 32-row half kk of the chunk: four column tiles of P, all of Q
+  struct Frags {
+    bf16x8 p[4], q[kSplit * NT];
+  };
+  auto read = [&](int buf, int kk, Frags& F) {
+    const u32x4* T = tiles + (kTwo ? buf * 2048 : 0) + w * 512;
+    const u32x4* const qtile = qtiles + (kTwo ? buf * kQ : 0);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 pa[2];
+    for (int b = 0; b < 4; ++b) {
+      s16x4 v[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        s16x4 v[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int m = 32 * kk + 8 * G + 4 * q + (j16 >> 2);
-          const int cc = 32 * (w & 1) + 16 * b + 4 * (j16 & 3);
-          v[q] = ds_read_tr(T, (m * 8 + ((cc >> 3) ^ g_swz(m))) * 8 + (cc & 7));
-        }
-        pa[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int q = 0; q < 2; ++q) {
+        const int m = 32 * kk + 8 * G + 4 * q + (j16 >> 2);
+        const int cc = 16 * b + 4 * (j16 & 3);
+        v[q] = ds_read_tr(T, (m * 8 + ((cc >> 3) ^ g_swz(m))) * 8 + (cc & 7));
       }
+      F.p[b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
 #pragma unroll
-      for (int p = 0; p < kSplit; ++p)
-#pragma unroll
-        for (int jt = 0; jt < NT; ++jt) {
-          const int rank = p * 16 * NT + 16 * jt + j16;
-          const bf16x8 qb = as_bf16x8(qtile[buf * kQ + rank * 8 + ((4 * kk + G) ^ ((rank >> 1) & 7))]);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) acc[b][jt] = kTR ? mfma16(qb, pa[b], acc[b][jt]) : mfma16(pa[b], qb, acc[b][jt]);
-        }
+    for (int i = 0; i < kSplit * NT; ++i) {
+      const int rank = 16 * i + j16;           // of the 3 x 16 NT
+      F.q[i] = as_bf16x8(qtile[rank * 8 + ((4 * kk + G) ^ ((rank >> 1) & 7))]);
     }
   };
-  // chunk i of the item is in set i % 2; loads past the end repeat the last chunk
+  auto multiply = [&](const Frags& F) {
+#pragma unroll
+    for (int i = 0; i < kSplit * NT; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        acc[b][i % NT] = kTR ? mfma16(F.p[b], F.q[i], acc[b][i % NT]) : mfma16(F.q[i], F.p[b], acc[b][i % NT]);
+  };
+  auto compute = [&](int buf) {
+    if constexpr (NT <= 4) {
+      Frags F0, F1;
+      read(buf, 0, F0);
+      read(buf, 1, F1);
+      multiply(F0);
+      multiply(F1);
+    } else {                                   // the operands of one half fill the registers
+      Frags F;
+      read(buf, 0, F);
+      multiply(F);
+      read(buf, 1, F);
+      multiply(F);
+    }
+  };
+  // Chunk i of the item is in set i % 2; loads past the end repeat the last
+  // chunk. The row numbers of a chunk are asked for before the loads of the
+  // chunk before it: waiting for them then leaves those loads in flight (asked
+  // for after them, every step waited for all its loads, 2.8 us a chunk).
   Regs R0, R1;
-  int rows[kPer];
+  int ra[kPer], rb[kPer];
   const int last = it.c1 - 1;
   auto at = [&](int ch) { return ch <= last ? ch : last; };
-  rows_of(it.c0, rows);
-  load(it.c0, rows, R0);
-  rows_of(at(it.c0 + 1), rows);
-  load(at(it.c0 + 1), rows, R1);
-  rows_of(at(it.c0 + 2), rows);
-  auto step = [&](int ch, Regs& R) {
-    const int buf = (ch - it.c0) & 1;
-    store(R, buf);                             // its last readers passed the barrier of the chunk before
+  rows_of(it.c0, ra);
+  rows_of(at(it.c0 + 1), rb);
+  load(it.c0, ra, R0);
+  __builtin_amdgcn_sched_barrier(0);
+  rows_of(at(it.c0 + 2), ra);
+  __builtin_amdgcn_sched_barrier(0);
+  load(at(it.c0 + 1), rb, R1);
+  __builtin_amdgcn_sched_barrier(0);
+  auto barrier = [&] { lds_barrier_on(tiles, qtiles, tiles, qtiles); };   // LDS done; loads stay in flight
+  auto next_loads = [&](int ch, const int (&rows)[kPer], int (&rows_next)[kPer], Regs& R) {
     __builtin_amdgcn_sched_barrier(0);
-    load(at(ch + 2), rows, R);
-    rows_of(at(ch + 3), rows);
+    rows_of(at(ch + 1), rows_next);
     __builtin_amdgcn_sched_barrier(0);
-    lds_barrier_on(tile, qtile, tile, qtile);  // this wave's LDS writes done; the loads stay in flight
-    compute(buf);
+    load(at(ch), rows, R);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  for (int ch = it.c0; ch < it.c1; ch += 2) {
-    step(ch, R0);
-    if (ch + 1 < it.c1) step(ch + 1, R1);
+  if constexpr (kTwo) {
+    // one workgroup per CU: chunk ch + 1 is written into the other buffers
+    // while chunk ch is multiplied
+    store(R0, 0);
+    next_loads(it.c0 + 2, ra, rb, R0);
+    barrier();
+    // a chunk: its first operands; then its products, the reads of the second
+    // half and the decode and writes of the next chunk between them (one wave
+    // per SIMD: nothing else would cover the LDS latency)
+    auto step = [&](int buf, const Regs& next) {
+      if constexpr (NT > 4) {
+        store(next, buf ^ 1);
+        compute(buf);
+        return;
+      }
+      Frags F0, F1;
+      read(buf, 0, F0);
+      __builtin_amdgcn_sched_barrier(0);
+      read(buf, 1, F1);
+      multiply(F0);
+      store(next, buf ^ 1);
+      multiply(F1);
+#pragma unroll
+      for (int i = 0; i < 8 * kSplit * NT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+        if (i < 4 * kSplit * NT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);               // VALU
+        if (i % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);            // LDS write
+      }
+    };
+    for (int ch = it.c0; ch < it.c1; ch += 2) {
+      step(0, R1);
+      next_loads(ch + 3, rb, ra, R1);
+      barrier();
+      if (ch + 1 < it.c1) {
+        step(1, R0);
+        next_loads(ch + 4, ra, rb, R0);
+        barrier();
+      }
+    }
+  } else {
+    for (int ch = it.c0; ch < it.c1; ch += 2) {
+      barrier();                               // the reads of the chunk before are done
+      store(R0, 0);
+      next_loads(ch + 2, ra, rb, R0);
+      barrier();
+      compute(0);
+      if (ch + 1 < it.c1) {
+        barrier();
+        store(R1, 0);
+        next_loads(ch + 3, rb, ra, R1);
+        barrier();
+        compute(0);
+      }
+    }
   }
 
+  // with more items than one: the sums go out whole, and the last workgroup
+  // of the column tile takes them back in item order
   float* const out = (kTR ? A.dA : A.dB) + static_cast<int64_t>(it.adapter) * C * r;
   const float s = A.scale ? A.scale[it.adapter] : A.alpha_r;
-  const bool direct = it.slot < 0;
-  float* const dst = direct ? out : (kTR ? A.partA : A.partB) + static_cast<int64_t>(it.slot) * C * r;
+  if (it.slot >= 0) {
+    constexpr int kBytes = kGCols * 16 * NT * 4;
+    auto part = [&](int slot) {
+      return part_rsrc(A.part + (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(slot)) * gridDim.x + blockIdx.x) *
+                                    (kBytes / 4), kBytes);
+    };
+    const __amdgpu_buffer_rsrc_t mine = part(it.slot);
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
-    for (int jt = 0; jt < NT; ++jt)
+      for (int jt = 0; jt < NT; ++jt) put_part(mine, (b * NT + jt) * kGThreads + t, acc[b][jt]);
+    if (!arrived_last(A.cnt2 + static_cast<int64_t>(it.slot0) * gridDim.x + blockIdx.x, it.items, t,
+                      reinterpret_cast<int*>(tiles)))
+      return;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int cc = c0 + 32 * w + 16 * b + (kTR ? j16 : 4 * G + v);
-        const int j = 16 * jt + (kTR ? 4 * G + v : j16);
-        if (j < r && cc < C) {
-          float* o = kTR ? dst + static_cast<int64_t>(j) * C + cc : dst + static_cast<int64_t>(cc) * r + j;
-          if (direct) *o = A.accumulate ? *o + s * acc[b][jt][v] : s * acc[b][jt][v];
-          else __hip_atomic_store(o, acc[b][jt][v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-      }
-  if (direct) return;
-  if (!arrived_last(A.cnt2 + static_cast<int64_t>(it.slot0) * gridDim.x + blockIdx.x, it.items, t, reinterpret_cast<int*>(tile))) return;
-  // the adapter's partials in item order, four values at a time (C % 8 == 0)
-  const int cols = C - c0 < kGCols ? C - c0 : kGCols;
-  for (int e = 4 * t; e < cols * r; e += 4 * kGThreads) {
-    const int64_t at4 = kTR ? static_cast<int64_t>(e / cols) * C + c0 + e % cols : static_cast<int64_t>(c0) * r + e;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < it.items; i0 += 8) {
-      f32x4 v[8];
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = __builtin_amdgcn_readfirstlane(it.slot0 + (i0 + u < it.items ? i0 + u : i0));
-        const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
-            (kTR ? A.partA : A.partB) + static_cast<int64_t>(i) * C * r, 0, C * r * 4, 0x00020000);
-        v[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(prs, static_cast<uint32_t>(at4 * 4), 0, 16));
-      }
+      for (int jt = 0; jt < NT; ++jt) acc[b][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < it.items; ++i) {
+      const __amdgpu_buffer_rsrc_t other = part(it.slot0 + i);
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (i0 + u < it.items) sum += v[u];
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int jt = 0; jt < NT; ++jt) acc[b][jt] += get_part(other, (b * NT + jt) * kGThreads + t);
     }
-    f32x4* o = reinterpret_cast<f32x4*>(out + at4);
-    sum *= s;
-    *o = A.accumulate ? *o + sum : sum;
   }
+  // a lane has four neighbours of one row of the output
+  const bool wide = kTR || r % 4 == 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int jt = 0; jt < NT; ++jt) {
+      const int cc = c0 + 64 * w + 16 * b + (kTR ? 4 * G : j16);
+      const int j = 16 * jt + (kTR ? j16 : 4 * G);
+      if (j >= r || cc >= C) continue;
+      float* const o = kTR ? out + static_cast<int64_t>(j) * C + cc : out + static_cast<int64_t>(cc) * r + j;
+      const f32x4 v = acc[b][jt] * s;
+      if (wide) {
+        f32x4* const o4 = reinterpret_cast<f32x4*>(o);
+        *o4 = A.accumulate ? *o4 + v : v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q < r) o[q] = A.accumulate ? o[q] + v[q] : v[q];
+      }
+    }
 }
 
 }  // namespace
@@ -899,11 +1030,11 @@ __device__ __forceinline__ void grad_item(const MgArgs& A, const GradItem& it, c
 // are cleared (unless they are added to), every gridDim.y - items'th adapter.
 template <int NT, int XF>
 __global__ __launch_bounds__(kGThreads) void k_mgrad(MgArgs A, GradLists L) {
-  __shared__ u32x4 tile[2 * 2048];
-  __shared__ u32x4 qtile[2 * kSplit * 16 * NT * 8];
+  __shared__ u32x4 tile[(mg_two<NT>() ? 2 : 1) * 2048];
+  __shared__ u32x4 qtile[(mg_two<NT>() ? 2 : 1) * kSplit * 16 * NT * 8];
   const bool is_b = static_cast<int>(blockIdx.x) < A.ctb;
   GradItem it;
-  if (L.rows) {
+  if (L.total) {
     const int items = L.total[1];
     if (static_cast<int>(blockIdx.y) >= items) {
       if (A.accumulate) return;
@@ -937,18 +1068,18 @@ __global__ __launch_bounds__(kGThreads) void k_mgrad(MgArgs A, GradLists L) {
 // ---------------------------------------------------------------------------
 // Row blocks of 64 (an adapter's operands are then read once for 64 rows) where
 // there are enough of them, else of 16; the contraction is split, and the
-// adapters of a row block dealt out, while that leaves at most one workgroup
-// per CU.
+// adapters of a row block dealt out, while that leaves at most one workgroup per
+// CU (t of 4096 rows, 4096 deep: 33, 22, 16 and 23 us in 64, 128, 256 and 512).
 MultiDownPlan multi_down_plan(int64_t M, int64_t Kc, int r, int n) {
   MultiDownPlan p;
   p.RM = M >= 1024 ? 4 : 1;
   p.blocks = cdiv(M, 16 * p.RM);
   const int64_t nchunk = cdiv(Kc, 64);
-  int64_t y = p.RM == 1 ? 256 / p.blocks : 1;
+  int64_t y = p.RM == 1 ? 512 / p.blocks : 1;
   y = std::min<int64_t>(std::min<int64_t>(y, 16), std::min<int64_t>(n, M));
   p.Y = std::max<int64_t>(y, 1);
   int64_t s = 256 / (p.blocks * p.Y);
-  s = std::min(s, cdiv(nchunk, p.RM == 1 ? 4 * kMdWaves : kMdWaves));   // a round of chunks per wave
+  s = std::min(s, cdiv(nchunk, p.RM == 1 ? 4 * kMdWaves : 2 * kMdWaves));   // about a round of chunks per wave
   p.S = std::max<int64_t>(std::min<int64_t>(s, kMdMaxSplit), 1);
   if (p.S > 1 || p.Y > 1) p.part_bytes = align256(static_cast<size_t>(p.blocks * p.S * p.RM * down_nt(r)) * 1024);
   return p;
@@ -1000,9 +1131,10 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   const int64_t used = listed ? std::min<int64_t>(M, n) : 0;       // adapters that can have rows
   g.chunks = listed ? M / 64 + used : full;                        // at most, with each adapter's last chunk partial
   g.Mp = g.chunks * 64;
-  // t and u: about two workgroups per CU, each chunk's split between them by
+  // t and u: about one workgroup per CU (more splits cost more than they
+  // hide: 4096 rows at 11008 x 4096 29 us with 4, 43 with 14), each chunk's split between them by
   // their lengths, at least a 64-deep piece per wave
-  const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(512 / g.chunks, 2);
+  const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(288 / g.chunks, 2);
   auto splits = [&](int64_t want, int64_t pieces) {
     return std::max<int64_t>(std::min({want, cdiv(pieces, kMdWaves), int64_t{kMdMaxSplit}}), 1);
   };
@@ -1021,8 +1153,8 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
     off += align256(bytes);
     return o;
   };
+  g.rows_off = take(static_cast<size_t>(g.Mp) * 4);
   if (listed) {
-    g.rows_off = take(static_cast<size_t>(g.Mp) * 4);
     g.chunk_off = take(static_cast<size_t>(g.chunks) * 4);
     g.item_off = take(static_cast<size_t>(g.items) * sizeof(GradItem));
     g.adapter_off = take(static_cast<size_t>(n) * sizeof(GradAdapter));
@@ -1033,8 +1165,7 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   g.tt_off = take(qb);
   g.ut_off = take(qb);
   g.dp_off = take(g.St > 1 || g.Su > 1 ? static_cast<size_t>(2 * g.chunks * kMdMaxSplit * 4 * g.nt) * 1024 : 0);
-  g.pa_off = take(static_cast<size_t>(g.slots) * K * r * 4);
-  g.pb_off = take(static_cast<size_t>(g.slots) * N * r * 4);
+  g.part_off = take(static_cast<size_t>(g.slots * ct) * kGCols * 16 * g.nt * 4);
   g.total = off;
   return g;
 }
@@ -1048,8 +1179,8 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   const int ctb = static_cast<int>(cdiv(N, kGCols)), cta = static_cast<int>(cdiv(K, kGCols));
   const bool find = index && M <= kFindMaxM;
   GradLists L{};
+  L.rows = reinterpret_cast<int*>(wsb + g.rows_off);
   if (index) {
-    L.rows = reinterpret_cast<int*>(wsb + g.rows_off);
     L.chunk_adapter = reinterpret_cast<int*>(wsb + g.chunk_off);
     L.item = reinterpret_cast<GradItem*>(wsb + g.item_off);
     L.adapter = reinterpret_cast<GradAdapter*>(wsb + g.adapter_off);
@@ -1071,7 +1202,6 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   d.cnt = reinterpret_cast<unsigned*>(wsb);
   d.cnt2 = reinterpret_cast<unsigned*>(wsb + g.cnt2_off);
   d.M = M;
-  d.Mp = g.Mp;
   d.N = static_cast<int>(N);
   d.K = static_cast<int>(K);
   d.r = r;
@@ -1080,7 +1210,7 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   d.St = static_cast<int>(g.St);
   d.Su = static_cast<int>(g.Su);
   d.ncnt2 = static_cast<int>(g.slots * (ctb + cta));
-  d.find = find;
+  d.mode = find ? kGdFind : index ? kGdListed : kGdWhole;
   MgArgs m{};
   m.x = x;
   m.tops = tops;
@@ -1088,13 +1218,11 @@ hipError_t launch_multi_grad(const void* x, const uint16_t* tops, int xfmt, cons
   m.tt = d.tt;
   m.ut = d.ut;
   m.scale = scale;
-  m.partA = reinterpret_cast<float*>(wsb + g.pa_off);
-  m.partB = reinterpret_cast<float*>(wsb + g.pb_off);
+  m.part = reinterpret_cast<float*>(wsb + g.part_off);
   m.dA = dA;
   m.dB = dB;
   m.cnt2 = d.cnt2;
   m.M = M;
-  m.Mp = g.Mp;
   m.alpha_r = alpha_r;
   m.N = d.N;
   m.K = d.K;

@@ -25,7 +25,7 @@ hipError_t launch_mstream(const MsPlan& p, const uint16_t* x, int64_t M, int64_t
 // (in = dY, Kc = N, W = B) of every row with an adapter: bf16 [M][rank_pad(r)].
 // ws: the workspace (its counters); part: multi_down_plan().part_bytes of it.
 // frags (wrow): `in` copied into MFMA order too, `mtiles` tiles of 16 rows.
-constexpr int kMdMaxSplit = 8;
+constexpr int kMdMaxSplit = 16;
 struct MultiDownPlan {
   int64_t RM = 1, blocks = 0, S = 1, Y = 1;      // 16-row tiles per block, blocks, splits, adapter shares
   size_t part_bytes = 0;

@@ -1173,7 +1173,7 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
 // e.g. 700 rows at 4096 x 11008: streaming 127 (3 rounds), tiled in five ranges
 // 88; 256 rows at 4096 x 4096: streaming 24, tiled 38.
 struct MultiPlan {
-  bool stream = false;
+  bool one = false, stream = false;
   int64_t S = 1;
   size_t t_off = 0, down_off = 0, part_off = 0, total = 0;   // the tiled kernels' workspace
 };
@@ -1181,6 +1181,11 @@ static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int 
   MultiPlan p;
   const int64_t Kc = op == 0 ? K : N, cols = op == 0 ? N : K;
   const int64_t tiles = cdiv(M, kTile) * cdiv(cols, kTile), steps = cdiv(Kc, 64);
+  if (op == 0 && M <= kMoMaxM) {
+    p.one = true;
+    p.total = kWsCounterBytes + mo_plan(M, N, K).part_bytes;
+    return p;
+  }
   double best = 0;
   for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 8)); ++S) {
     double us = static_cast<double>(cdiv(S * tiles, 256)) * (1.4 * 4 * cdiv(cdiv(steps, 4), S) + 8);
@@ -1222,6 +1227,8 @@ hipError_t launch_multi_fwd(const uint16_t* x, int64_t M, int64_t N, int64_t K, 
   const MultiPlan p = multi_plan(0, M, N, K, r, n);
   char* wsb = static_cast<char*>(ws);
   const MultiLora ml{index, scale, n, static_cast<int>(p.S), reinterpret_cast<float*>(wsb + p.part_off)};
+  if (p.one)
+    return launch_mone(mo_plan(M, N, K), x, M, N, K, packed, qscale, step, A, B, ml, r, y, ws, cb, stream);
   if (p.stream)
     return launch_mstream(ms_plan(M, N, K, r, n), x, M, N, K, packed, qscale, step, A, B, ml, r, y, ws, cb, stream);
   uint16_t* tl = reinterpret_cast<uint16_t*>(wsb + p.t_off);

@@ -16,6 +16,15 @@ struct MsPlan {
   int64_t mblocks = 1, S = 1;
   size_t t_off = 0, x_off = 0, down_off = 0, part_off = 0, total = 0;
 };
+constexpr int64_t kMoMaxM = 4;                   // rows the one-launch forward takes
+struct MoPlan {
+  int64_t blocks = 1, S = 1;                     // blocks of 64 weight rows, ranges of K
+  size_t part_bytes = 0;
+};
+MoPlan mo_plan(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mone(const MoPlan& p, const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
+                       const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,
+                       const MultiLora& ml, int r, uint16_t* y, void* ws, const Codebook& cb, hipStream_t stream);
 MsPlan ms_plan(int64_t M, int64_t N, int64_t K, int r, int n);
 hipError_t launch_mstream(const MsPlan& p, const uint16_t* x, int64_t M, int64_t N, int64_t K, const uint8_t* packed,
                           const int8_t* qscale, const float* step, const uint16_t* A, const uint16_t* B,

@@ -1195,7 +1195,7 @@ static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int 
   if (op == 0 && M <= kMsMaxM) {
     const MsPlan m = ms_plan(M, N, K, r, n);
     const int64_t items = cdiv(N, 64) * m.mblocks * m.S;
-    const double us = static_cast<double>(cdiv(items, m.MT <= 2 ? 512 : 256)) * (9 + 2.8 * cdiv(cdiv(K, 256), 4 * m.S));
+    const double us = static_cast<double>(cdiv(items, 256)) * (9 + 2.8 * cdiv(cdiv(K, 256), 4 * m.S));
     if (us <= best) {
       p.stream = true;
       p.total = m.total;

@@ -48,7 +48,7 @@ struct MsArgs {
   const float* step;
   const uint16_t* B;        // [n][N][r]
   uint16_t* y;
-  float* part;              // [item][16 MT][64]
+  float* part;              // [row block of W, block of x rows][S][16 MT x 64]
   unsigned* cnt;            // one per (row block of W, block of x rows)
   int M, N, K, r, rp, S, mblocks, items;
 };
@@ -239,75 +239,48 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
     }
   }
 
-  // y (or, with a split K, first the partial sums): 16 MT rows x 64 columns
+  // with a split K: the partial sums, which the last range to arrive adds in order
+  if (P.S > 1) {
+    constexpr int kPart = MT * 256;              // groups of four
+    const __amdgpu_buffer_rsrc_t part = part_rsrc(
+        P.part + static_cast<int64_t>(nb * P.mblocks + mb) * P.S * (kPart * 4), P.S * kPart * 16);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) put_part(part, s * kPart + i * 256 + t, sum[i]);
+    if (!arrived_last(P.cnt + nb * P.mblocks + mb, P.S, t, &last_flag)) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      f32x4 v[kMsMaxSplit];
+#pragma unroll
+      for (int u = 0; u < kMsMaxSplit; ++u) v[u] = get_part(part, u * kPart + i * 256 + t);   // past S: zero
+      sum[i] = v[0];
+#pragma unroll
+      for (int u = 1; u < kMsMaxSplit; ++u)
+        if (u < P.S) sum[i] += v[u];
+    }
+  }
+  // y: 16 MT rows x 64 columns, through LDS to whole 16-byte pieces
   const int mrows = P.M - 16 * mt0 < 16 * MT ? P.M - 16 * mt0 : 16 * MT;
   uint16_t* const yb = P.y + static_cast<int64_t>(16 * mt0) * N + n0;
   const int ncols = N - n0 < kMsRows ? N - n0 : kMsRows;
-  if (P.S == 1) {
-    __syncthreads();                             // every wave has read its sums
-    uint16_t* const tile = reinterpret_cast<uint16_t*>(red);
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) tile[(16 * i + 4 * g + v) * 72 + 16 * w + c] = bf16_bits(sum[i][v]);
-    __syncthreads();
-    const bool wide = ncols == kMsRows && N % 8 == 0;
-    for (int e = t; e < mrows * 8; e += 256) {
-      const int row = e >> 3, col = 8 * (e & 7);
-      const uint16_t* src = tile + row * 72 + col;
-      uint16_t* dst = yb + static_cast<int64_t>(row) * N + col;
-      if (wide) {
-        *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
-      } else {
-        for (int q = 0; q < 8; ++q)
-          if (col + q < ncols) dst[q] = src[q];
-      }
-    }
-    return;
-  }
-  // the partials and the counter go through device-scope accesses, coherent
-  // across the XCDs' caches without flushing them; every wave waits for its own
-  // stores before the workgroup counts itself in
-  constexpr int kPart = 16 * MT * kMsRows;
-  float* const mine = P.part + (static_cast<int64_t>(nb * P.mblocks + mb) * P.S + s) * kPart;
+  __syncthreads();                               // every wave has read its sums
+  uint16_t* const tile = reinterpret_cast<uint16_t*>(red);
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = 16 * i + 4 * g + v;
-      if (row < mrows)
-        __hip_atomic_store(mine + row * kMsRows + 16 * w + c, sum[i][v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0);
+    for (int v = 0; v < 4; ++v) tile[(16 * i + 4 * g + v) * 72 + 16 * w + c] = bf16_bits(sum[i][v]);
   __syncthreads();
-  unsigned* const cnt = P.cnt + nb * P.mblocks + mb;
-  if (t == 0) {
-    const unsigned old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last_flag = old == static_cast<unsigned>(P.S - 1);
-  }
-  __syncthreads();
-  if (!last_flag) return;
-  const __amdgpu_buffer_rsrc_t prs = __builtin_amdgcn_make_buffer_rsrc(
-      P.part + static_cast<int64_t>(nb * P.mblocks + mb) * P.S * kPart, 0, P.S * kPart * 4, 0x00020000);
-  for (int e = t; e < mrows * 16; e += 256) {
-    const int row = e >> 4, col = 4 * (e & 15);
-    f32x4 v[kMsMaxSplit];
-#pragma unroll
-    for (int u = 0; u < kMsMaxSplit; ++u)
-      if (u < P.S)
-        v[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             prs, static_cast<uint32_t>((u * kPart + row * kMsRows + col) * 4), 0, 16));
-    f32x4 out = v[0];
-#pragma unroll
-    for (int u = 1; u < kMsMaxSplit; ++u)
-      if (u < P.S) out += v[u];
+  const bool wide = ncols == kMsRows && N % 8 == 0;
+  for (int e = t; e < mrows * 8; e += 256) {
+    const int row = e >> 3, col = 8 * (e & 7);
+    const uint16_t* src = tile + row * 72 + col;
     uint16_t* dst = yb + static_cast<int64_t>(row) * N + col;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (col + q < ncols) dst[q] = bf16_bits(out[q]);
+    if (wide) {
+      *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
+    } else {
+      for (int q = 0; q < 8; ++q)
+        if (col + q < ncols) dst[q] = src[q];
+    }
   }
-  if (t == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------------------
@@ -500,17 +473,16 @@ __global__ __launch_bounds__(256, 2) void k_mone(MoArgs P, MultiLora ml, Codeboo
 }  // namespace
 
 // Items: blocks of 64 weight rows x blocks of 16 MT rows of x (MT up to 4) x S
-// ranges of K. S is the most that keeps every item resident at once (two
-// workgroups per CU up to MT = 2, one above; a second round costs a whole item:
-// 48 rows at 11008 x 4096 take 21 us with S = 1, 29 with 2, 35 with 3) and
-// leaves every wave a super-step.
+// ranges of K. S is the most that gives every CU at most one item and every
+// wave a super-step (11008 x 4096, ranges 1 / 2 / 4: 16 rows 16.9 / 19.2 / 19.5
+// us, 48 rows 20.8 / 27.5 / 30.9; 4096 x 4096, 32 rows 16.5 / 13.9 / 12.5).
 MsPlan ms_plan(int64_t M, int64_t N, int64_t K, int r, int n) {
   MsPlan p;
   const int64_t mtiles = cdiv(M, 16), nss = cdiv(K, 256);
   p.MT = static_cast<int>(mtiles < 4 ? mtiles : 4);
   p.mblocks = cdiv(mtiles, p.MT);
   const int64_t blocks = cdiv(N, kMsRows) * p.mblocks;
-  int64_t S = (p.MT <= 2 ? 512 : 256) / blocks;
+  int64_t S = 256 / blocks;
   if (S > cdiv(nss, 4)) S = cdiv(nss, 4);
   if (S > kMsMaxSplit) S = kMsMaxSplit;
   p.S = S < 1 ? 1 : S;
@@ -532,8 +504,8 @@ MoPlan mo_plan(int64_t M, int64_t N, int64_t K) {
   MoPlan p;
   const int64_t nss = cdiv(K, 256);
   p.blocks = cdiv(N, kMsRows);
-  // two workgroups per CU, and a super-step per wave
-  p.S = std::max<int64_t>(std::min({512 / p.blocks, cdiv(nss, 4), int64_t{kMsMaxSplit}}), 1);
+  // as ms_plan
+  p.S = std::max<int64_t>(std::min({256 / p.blocks, cdiv(nss, 4), int64_t{kMsMaxSplit}}), 1);
   if (p.S > 1) p.part_bytes = static_cast<size_t>(p.blocks * p.S) * 4096;
   return p;
 }

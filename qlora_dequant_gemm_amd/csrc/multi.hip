@@ -47,21 +47,22 @@ struct MdArgs {
   const uint16_t* in;       // [M][Kc]
   const uint16_t* W;        // [n][r Kc]
   uint16_t* out;            // [M][rp]
-  float* part;              // [blocks][S][16 RT x 16 RM]
+  float* part;              // [blocks][Smax][16 RT x 16 RM]
   unsigned* cnt;
   u32x4* frags;
   int64_t M, nfrag;
-  int Kc, r, rp, blocks, S, Y;
+  int Kc, r, rp, blocks, Q, Smax;
 };
 
 // s_a t (kBT false: in = x, W = A) or s_a u (kBT true: in = dY, W = B), rounded
 // to bf16 once, [M][rp] with the ranks past r zero; rows without an adapter are
 // not written. (One bf16 number each, as for a single adapter: the output is
 // bf16 itself. The scale goes in before the rounding, so that the GEMMs need
-// no scale.) A workgroup has 16 RM rows, one of S ranges of the contraction and
-// every Y-th of the adapters among its rows, one pass each (rows of a request
-// follow each other, so mostly one pass); with S or Y above 1 the passes leave
-// partial sums and the last workgroup of the row block adds them in order.
+// no scale.) A row block of 16 RM rows has Q workgroups. They share its passes,
+// one for each of the D adapters among its rows (mostly one: rows of a request
+// follow each other), and, where there are more workgroups than passes, split
+// the contraction into S = Q / D ranges: those leave partial sums, and the last
+// workgroup of the block adds them in order.
 // Workgroups past those copy x into MFMA order: fragment (tile, ss, j) has, at
 // lane (g, c), columns 256 ss + 64 g + 8 j + (0 2 | 4 6 | 1 3 | 5 7) of row 16
 // tile + c, zero past M and Kc.
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int c = lane & 15;
   const int Kc = P.Kc, r = P.r, rp = P.rp;
-  const int wgs = P.blocks * P.S * P.Y;
+  const int wgs = P.blocks * P.Q;
   if (static_cast<int>(blockIdx.x) >= wgs) {
     if constexpr (!kBT) {
       const int nss = (Kc + 255) / 256;
@@ -89,28 +90,34 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
   }
   __shared__ u32x4 lds[md_lds<RM, RT, kBT>()];
   __shared__ int flag;
-  const int block = blockIdx.x / (P.S * P.Y), s = (blockIdx.x / P.Y) % P.S, y = blockIdx.x % P.Y;
-  const int nchunk = (Kc + 63) / 64;
-  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / P.S);
-  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / P.S);
+  const int block = blockIdx.x / P.Q, q = blockIdx.x % P.Q;
   const int64_t m0 = static_cast<int64_t>(block) * 16 * RM;
   // the rows' adapters: row lane of the block (RM == 1: lanes 0 .. 15)
   int id = lane < 16 * RM && m0 + lane < P.M ? ml.index[m0 + lane] : -1;
   if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
   const uint64_t any = __ballot(id >= 0);
   if (!any) return;                              // the whole row block: nobody counts
+  int D = 0;
+  for (uint64_t pend = any; pend; ++D) pend &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(pend)));
+  int S = P.Q / D < P.Smax ? P.Q / D : P.Smax;
+  if (S < 1) S = 1;
+  // ranges: workgroup q has range q % S of pass q / S; one range: passes q, q + Q, ...
+  const bool direct = S == 1;
+  const int y = direct ? q : q / S, step = direct ? P.Q : D, s = direct ? 0 : q % S;
+  const int nchunk = (Kc + 63) / 64;
+  const int qb = static_cast<int>(static_cast<int64_t>(nchunk) * s / S);
+  const int qe = static_cast<int>(static_cast<int64_t>(nchunk) * (s + 1) / S);
   uint64_t pend = any;
-  const bool direct = P.S == 1 && P.Y == 1;
   constexpr int kCount = RM * RT * 64;           // groups of four partial sums
   const __amdgpu_buffer_rsrc_t part =
-      part_rsrc(P.part + static_cast<int64_t>(block) * P.S * kCount * 4, P.S * kCount * 16);
+      part_rsrc(P.part + static_cast<int64_t>(block) * P.Smax * kCount * 4, S * kCount * 16);
   f32x4* const red = reinterpret_cast<f32x4*>(lds);
   constexpr int kPerWave = md_lds<RM, RT, kBT>() / kMdWaves;
   for (int ord = 0; pend; ++ord) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(pend));
     const uint64_t mine = __ballot(id == a);
     pend &= ~mine;
-    if (ord % P.Y != y) continue;
+    if (ord % step != y) continue;
     int64_t rows[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) rows[i] = (mine >> (16 * i + c)) & 1 ? m0 + 16 * i + c : -1;
@@ -148,8 +155,8 @@ __global__ __launch_bounds__(64 * kMdWaves) void k_mdown(MdArgs P, MultiLora ml)
     __syncthreads();
   }
   if (direct) return;
-  if (!arrived_last(P.cnt + block, P.S * P.Y, t, &flag)) return;
-  sum_partials<RM, RT>(part, P.S, t, [&](int, int row, int j, const f32x4& v) {
+  if (!arrived_last(P.cnt + block, P.Q, t, &flag)) return;
+  sum_partials<RM, RT>(part, S, t, [&](int, int row, int j, const f32x4& v) {
     if (j >= rp) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -795,21 +802,21 @@ __global__ __launch_bounds__(kGThreads) void k_mgrad(MgArgs A, GradLists L) {
 // host side
 // ---------------------------------------------------------------------------
 // Row blocks of 64 (an adapter's operands are then read once for 64 rows) where
-// there are enough of them, else of 16; the contraction is split, and the
-// adapters of a row block dealt out, while that leaves at most one workgroup per
-// CU (t of 4096 rows, 4096 deep: 33, 22, 16 and 23 us in 64, 128, 256 and 512).
+// there are enough of them, else of 16. Q: one workgroup per CU in all with
+// blocks of 64 (t of 4096 rows, 4096 deep: 33, 22, 16 and 23 us in 64, 128, 256
+// and 512), two with blocks of 16, whose rows may have 16 adapters.
 MultiDownPlan multi_down_plan(int64_t M, int64_t Kc, int r, int n) {
   MultiDownPlan p;
   p.RM = M >= 1024 ? 4 : 1;
   p.blocks = cdiv(M, 16 * p.RM);
-  const int64_t nchunk = cdiv(Kc, 64);
-  int64_t y = p.RM == 1 ? 512 / p.blocks : 1;
-  y = std::min<int64_t>(std::min<int64_t>(y, 16), std::min<int64_t>(n, M));
-  p.Y = std::max<int64_t>(y, 1);
-  int64_t s = 256 / (p.blocks * p.Y);
-  s = std::min(s, cdiv(nchunk, p.RM == 1 ? 4 * kMdWaves : 2 * kMdWaves));   // about a round of chunks per wave
-  p.S = std::max<int64_t>(std::min<int64_t>(s, kMdMaxSplit), 1);
-  if (p.S > 1 || p.Y > 1) p.part_bytes = align256(static_cast<size_t>(p.blocks * p.S * p.RM * down_nt(r)) * 1024);
+  // ranges of at least a round of chunks per wave; a workgroup more than
+  // passes times ranges has nothing to do
+  const int64_t round = p.RM == 1 ? 4 * kMdWaves : 2 * kMdWaves;
+  p.Smax = std::max<int64_t>(std::min<int64_t>(cdiv(cdiv(Kc, 64), round), kMdMaxSplit), 1);
+  const int64_t passes = std::min<int64_t>({n, M, 16 * p.RM});
+  p.Q = std::max<int64_t>(std::min((p.RM == 1 ? 512 : 256) / p.blocks, passes * p.Smax), 1);
+  if (p.Smax > p.Q) p.Smax = p.Q;
+  if (p.Smax > 1) p.part_bytes = align256(static_cast<size_t>(p.blocks * p.Smax * p.RM * down_nt(r)) * 1024);
   return p;
 }
 
@@ -830,9 +837,9 @@ hipError_t launch_multi_down(bool wrow, const uint16_t* in, int64_t M, int64_t K
   a.r = r;
   a.rp = static_cast<int>(rank_pad(r));
   a.blocks = static_cast<int>(p.blocks);
-  a.S = static_cast<int>(p.S);
-  a.Y = static_cast<int>(p.Y);
-  const dim3 grid(static_cast<unsigned>(p.blocks * p.S * p.Y + cdiv(a.nfrag, kMdWaves))), block(64 * kMdWaves);
+  a.Q = static_cast<int>(p.Q);
+  a.Smax = static_cast<int>(p.Smax);
+  const dim3 grid(static_cast<unsigned>(p.blocks * p.Q + cdiv(a.nfrag, kMdWaves))), block(64 * kMdWaves);
 #define QNF4_MD2(RMV, RTV, BT) hipLaunchKernelGGL(HIP_KERNEL_NAME(k_mdown<RMV, RTV, BT>), grid, block, 0, stream, a, ml)
 #define QNF4_MD(RTV)                                 \
   do {                                               \

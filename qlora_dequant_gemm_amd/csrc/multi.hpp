@@ -36,7 +36,7 @@ hipError_t launch_mstream(const MsPlan& p, const uint16_t* x, int64_t M, int64_t
 // frags (wrow): `in` copied into MFMA order too, `mtiles` tiles of 16 rows.
 constexpr int kMdMaxSplit = 16;
 struct MultiDownPlan {
-  int64_t RM = 1, blocks = 0, S = 1, Y = 1;      // 16-row tiles per block, blocks, splits, adapter shares
+  int64_t RM = 1, blocks = 0, Q = 1, Smax = 1;   // 16-row tiles per block, blocks, workgroups of a block, ranges at most
   size_t part_bytes = 0;
 };
 MultiDownPlan multi_down_plan(int64_t M, int64_t Kc, int r, int n);

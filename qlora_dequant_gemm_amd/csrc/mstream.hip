@@ -56,11 +56,13 @@ struct MsArgs {
 // The adapter term of a 16 x 16 tile: lane (g, c) gets rows 4 g + v of column n.
 // id: the adapter of row c (lanes of all g alike), < 0 for none; tv(col, hi, lo): 8
 // values of t of row c from rank col (a multiple of 8), bf16. The B rows of up
-// to kMsBatch adapters are asked for together; a row takes the product with its
+// to kBatch adapters are asked for together; a row takes the product with its
 // own adapter's, chosen after it (a NaN in one adapter must not reach the rows
 // of another).
 // kLo: tv(col, hi, lo) gives t as two bf16 numbers.
-template <bool kLo, typename T>
+// kBatch: adapters at once (code that is run once is mostly fetched, not run:
+// no more of it than the rows can need).
+template <bool kLo, int kBatch, typename T>
 __device__ __forceinline__ f32x4 adapter_term(int id, const uint16_t* B, int N, int64_t n, int r, int lane, T&& tv) {
   const int g = lane >> 4;
   const bool vec = (r & 7) == 0;
@@ -68,22 +70,22 @@ __device__ __forceinline__ f32x4 adapter_term(int id, const uint16_t* B, int N, 
   f32x4 lora = {0.f, 0.f, 0.f, 0.f};
   uint32_t pend = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
   while (pend) {
-    uint32_t rows[kMsBatch];
-    int ad[kMsBatch];
+    uint32_t rows[kBatch];
+    int ad[kBatch];
 #pragma unroll
-    for (int u = 0; u < kMsBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       ad[u] = __builtin_amdgcn_readlane(id, pend ? __builtin_ctz(pend) : 0);
       rows[u] = pend ? static_cast<uint32_t>(__ballot(id == ad[u])) & 0xFFFFu : 0u;
       pend &= ~rows[u];
     }
-    f32x4 p[kMsBatch];
+    f32x4 p[kBatch];
 #pragma unroll
-    for (int u = 0; u < kMsBatch; ++u) p[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < kBatch; ++u) p[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < r; j0 += 32) {
       const int col = j0 + 8 * g;
-      u32x4 bf[kMsBatch];
+      u32x4 bf[kBatch];
 #pragma unroll
-      for (int u = 0; u < kMsBatch; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         if (!rows[u]) continue;
         const uint16_t* br = B + (static_cast<int64_t>(ad[u]) * N + n) * r;
         if (vec) bf[u] = ld16(br + (col < r ? col : 0));
@@ -92,7 +94,7 @@ __device__ __forceinline__ f32x4 adapter_term(int id, const uint16_t* B, int N, 
       u32x4 hi, lo;
       tv(col, hi, lo);
 #pragma unroll
-      for (int u = 0; u < kMsBatch; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         if (!rows[u]) continue;
         const bf16x8 b = as_bf16x8(col < r ? bf[u] : zero);
         p[u] = mfma16(as_bf16x8(col < r ? hi : zero), b, p[u]);
@@ -100,7 +102,7 @@ __device__ __forceinline__ f32x4 adapter_term(int id, const uint16_t* B, int N, 
       }
     }
 #pragma unroll
-    for (int u = 0; u < kMsBatch; ++u)
+    for (int u = 0; u < kBatch; ++u)
 #pragma unroll
       for (int v = 0; v < 4; ++v) lora[v] = (rows[u] >> (4 * g + v)) & 1u ? p[u][v] : lora[v];
   }
@@ -222,21 +224,29 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
   }
 
   // the adapter term of this wave's 16 columns: lane (g, c) has column n, rows
-  // 4 g + v of each tile
-  const int n = n0 + 16 * w + c;
+  // 4 g + v of each tile. The loop over the tiles stays rolled (its code is long
+  // and run once, so it is fetched for the first tile and run for the others);
+  // the terms wait in LDS.
+  __syncthreads();                               // every wave has read its sums
   {
+    const int n = n0 + 16 * w + c;
     const int64_t nr = n < N ? n : N - 1;
     const int r = P.r, rp = P.rp;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < MT; ++i) {
-      if ((mt0 + i) % P.S != s) continue;
+      int row_id = id[0];
+#pragma unroll
+      for (int k = 1; k < MT; ++k) row_id = i == k ? id[k] : row_id;
+      if ((mt0 + i) % P.S != s) row_id = -1;
       const int m = 16 * (mt0 + i) + c;
       const uint16_t* trow = P.t + static_cast<int64_t>(m < P.M ? m : P.M - 1) * rp;
-      const f32x4 lora = adapter_term<false>(id[i], P.B, N, nr, r, lane, [&](int col, u32x4& hi, u32x4&) {
-        hi = ld16(trow + (col < rp ? col : 0));
-      });
-      sum[i] += lora;
+      red[(w * MT + i) * 64 + lane] =
+          adapter_term<false, kMsBatch>(row_id, P.B, N, nr, r, lane, [&](int col, u32x4& hi, u32x4&) {
+            hi = ld16(trow + (col < rp ? col : 0));
+          });
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sum[i] += red[(w * MT + i) * 64 + lane];
   }
 
   // with a split K: the partial sums, which the last range to arrive adds in order
@@ -262,7 +272,7 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
   const int mrows = P.M - 16 * mt0 < 16 * MT ? P.M - 16 * mt0 : 16 * MT;
   uint16_t* const yb = P.y + static_cast<int64_t>(16 * mt0) * N + n0;
   const int ncols = N - n0 < kMsRows ? N - n0 : kMsRows;
-  __syncthreads();                               // every wave has read its sums
+  __syncthreads();                               // every wave has read its terms
   uint16_t* const tile = reinterpret_cast<uint16_t*>(red);
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -320,9 +330,7 @@ __global__ __launch_bounds__(256, 2) void k_mone(MoArgs P, MultiLora ml, Codeboo
   // items of a row block on one XCD
   const int item = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   if (item >= P.blocks * P.S) return;
-  int id = c < P.M ? ml.index[c] : -1;
-  if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
-  const uint32_t any = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
+  int id = c < P.M ? ml.index[c] : -1;           // looked at once the first weights are asked for
   const int s = item % P.S, nb = item / P.S;
   const int nbr = K / 64, nss = (nbr + 3) / 4;
   const int ss0 = static_cast<int>(static_cast<int64_t>(nss) * s / P.S);
@@ -374,11 +382,20 @@ __global__ __launch_bounds__(256, 2) void k_mone(MoArgs P, MultiLora ml, Codeboo
   for (int nt = 0; nt < kMsNT; ++nt) acc[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int jt = 0; jt < RT; ++jt) tacc[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int first = any ? __builtin_amdgcn_readlane(id, __builtin_ctz(any)) : 0;
   Step cur, nxt;
   int ss = ss0 + w;
-  if (ss < ss1) {
-    load(ss, cur);
+  load(ss < ss1 ? ss : ss0, cur);
+  __builtin_amdgcn_sched_barrier(0);
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(ml.n)) id = -1;
+  const uint32_t any = static_cast<uint32_t>(__ballot(id >= 0)) & 0xFFFFu;
+  const int first = any ? __builtin_amdgcn_readlane(id, __builtin_ctz(any)) : 0;
+  // the end's operands of the first adapter, brought near: nothing covers
+  // their latency there
+  const int n = nb * kMsRows + 16 * w + c;
+  const float scale0 = ml.scale[first];
+  uint32_t near = 0;
+  if (any) near = P.B[(static_cast<int64_t>(first) * N + (n < N ? n : N - 1)) * r];
+  {
     for (; ss < ss1; ss += 4) {
       const bool more = ss + 4 < ss1;
       const uint32_t kv = ss * 4 + g < nbr ? 0xFFFFFFFFu : 0u;
@@ -427,11 +444,11 @@ __global__ __launch_bounds__(256, 2) void k_mone(MoArgs P, MultiLora ml, Codeboo
   f32x4 sum = red[w * 64 + lane];
 #pragma unroll
   for (int ww = 1; ww < 4; ++ww) sum += red[(ww * kMsNT + w) * 64 + lane];
-  const int n = nb * kMsRows + 16 * w + c;
+  asm volatile("" ::"v"(near));
   if (any) {
     // t of row c from rank col: the waves' parts in order, times the row's scale
-    const float scale = id >= 0 ? ml.scale[id] : 0.f;
-    sum += adapter_term<true>(id, P.B, N, n < N ? n : N - 1, r, lane, [&](int col, u32x4& hi, u32x4& lo) {
+    const float scale = id < 0 ? 0.f : id == first ? scale0 : ml.scale[id];
+    sum += adapter_term<true, static_cast<int>(kMoMaxM)>(id, P.B, N, n < N ? n : N - 1, r, lane, [&](int col, u32x4& hi, u32x4& lo) {
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

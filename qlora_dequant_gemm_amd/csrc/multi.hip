@@ -868,17 +868,20 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   g.Mp = g.chunks * 64;
   // t and u: about one workgroup per CU (more splits cost more than they
   // hide: 4096 rows at 11008 x 4096 29 us with 4, 43 with 14), each chunk's split between them by
-  // their lengths, at least a 64-deep piece per wave
+  // their lengths, two 64-deep pieces and more per wave (513 rows, 4096 deep:
+  // 12.5 us in 16 ranges, 10.9 in 8, 11.3 in 4)
   const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(288 / g.chunks, 2);
   auto splits = [&](int64_t want, int64_t pieces) {
-    return std::max<int64_t>(std::min({want, cdiv(pieces, kMdWaves), int64_t{kMdMaxSplit}}), 1);
+    return std::max<int64_t>(std::min({want, cdiv(pieces, 2 * kMdWaves), int64_t{kMdMaxSplit}}), 1);
   };
   g.St = splits(std::max<int64_t>((q * nk + (nk + nn) / 2) / (nk + nn), 1), nk);
   g.Su = splits(q - std::min(q - 1, g.St), nn);
   // items: about two workgroups per CU over all column tiles; an item's
-  // partial sums (4 r bytes a column) stay small beside the rows it reads
+  // partial sums (4 r bytes a column) stay small beside the rows it reads (r 16,
+  // 513 rows: 8.6 us with items of two chunks, 10.2 of four; r 64, 4096 rows:
+  // 43 us of sixteen, 55 of eight)
   const int64_t ct = cdiv(N, kGCols) + cdiv(K, kGCols);
-  g.per_item = std::max<int64_t>({cdiv(full, cdiv(512, ct)), r / 4, 2});
+  g.per_item = std::max<int64_t>({cdiv(full, cdiv(512, ct)), r > 16 ? r / 4 : 2, 2});
   g.items = listed ? full / g.per_item + used : cdiv(full, g.per_item);
   // slots: an adapter of I >= 2 items has more than (I - 1) per_item full chunks
   g.slots = listed ? 2 * (full / g.per_item) : (g.items > 1 ? g.items : 0);

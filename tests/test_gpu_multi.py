@@ -170,7 +170,12 @@ SHAPES = [
 @pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(40, 37, 128, 8, 3, "runs"), (260, 301, 320, 12, 3, "mixed"),
                                                      (5, 1, 2112, 16, 2, "mixed"), (48, 200, 4160, 16, 30, "mixed"),
                                                      # a contraction split over workgroups: the tiled kernel, ragged and whole
-                                                     (1100, 264, 2112, 16, 6, "runs"), (1030, 520, 2048, 40, 40, "mixed")])
+                                                     (1100, 264, 2112, 16, 6, "runs"), (1030, 520, 2048, 40, 40, "mixed"),
+                                                     # its other rank groups; up to four rows
+                                                     (1100, 264, 320, 100, 3, "runs"), (1090, 40, 192, 24, 5, "mixed"),
+                                                     (1200, 520, 64, 80, 4, "runs"), (1, 4104, 1088, 100, 2, "one"),
+                                                     (2, 520, 4096, 64, 2, "mixed"), (4, 264, 2112, 33, 9, "mixed"),
+                                                     (3, 72, 64, 16, 3, "last"), (4, 136, 320, 16, 2, "none")])
 def test_forward(qops, M, N, K, r, n, kind):
     c = Case(qops, M, N, K, r, n, kind, 100 + M)
     c.check_fwd(qops.lora_fwd_multi(dev(c.x), c.qw, c.pool, c.index))
@@ -293,7 +298,7 @@ def test_checkpoint_shapes_and_buffers(qops):
 
 
 # ---------------------------------------------------------------------------
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [4, 8, 300, 1100])
 def test_bad_numbers_stay_with_their_rows(qops, M):
     """NaN and infinities in one adapter, its scale or a row of x reach only the
     rows and gradients that use them."""
@@ -357,7 +362,7 @@ def step(ops, c, x, dy, pool, index, ws, bufs):
     return y, kept, dx, dA, dB
 
 
-@pytest.mark.parametrize("M,kind", [(48, "mixed"), (333, "runs")])
+@pytest.mark.parametrize("M,kind", [(3, "mixed"), (48, "mixed"), (333, "runs"), (1100, "runs")])
 def test_a_step_eager_streams_and_replayed(qops, M, kind):
     c = Case(qops, M, 264, 320, 16, 5, kind, 41)
     x, dy = dev(c.x), dev(c.dy)

@@ -640,7 +640,9 @@ struct BCodes {
 // kMulti: Al is a pool [n][r][K]; row m uses adapter ml.index[m]; u carries the
 // scale. It also splits the contraction (ml.S > 1) as k_gemm_fwd does, in ranges
 // of whole step pairs; the o-th adapter of a tile is added by range o % S.
-template <int RSN, bool kMulti = false>
+// MB: 32-row blocks per wave; the tile has 64 MB rows (fewer than 256 where the
+// batch is short and the decode, not the MFMAs, bounds a step).
+template <int RSN, bool kMulti = false, int MB = 4>
 __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __restrict__ dy, int64_t M, int64_t N,
                                                             int64_t K, const uint8_t* __restrict__ packed,
                                                             const int8_t* __restrict__ qscale,
@@ -651,8 +653,9 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
                                                             MultiLora ml) {
   // the two W' buffers are one array: after the main loop it holds A's
   // slice for the LoRA epilogue (up to 128 ranks x 256 columns)
-  __shared__ u32x4 As0[kChunks];
-  __shared__ u32x4 As1[kChunks];
+  constexpr int kRows = 64 * MB;               // rows of the tile
+  __shared__ u32x4 As0[8 * kRows];
+  __shared__ u32x4 As1[8 * kRows];
   __shared__ u32x4 Ws[2 * kBwChunks];
   u32x4* const Ws0 = Ws;
   u32x4* const Ws1 = Ws + kBwChunks;
@@ -660,13 +663,13 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w >> 2, wn = w & 3;
   const int h = lane >> 5, l32 = lane & 31;
-  const int ntm = static_cast<int>(cdiv(M, kTile)), ntk = static_cast<int>(cdiv(K, kTile));
+  const int ntm = static_cast<int>(cdiv(M, kRows)), ntk = static_cast<int>(cdiv(K, kTile));
   int tm, tk;
   const int split = kMulti ? __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x) / (ntm * ntk)) : 0;
   tile_of(blockIdx.x - split * ntm * ntk, ntm, ntk, tm, tk);
   tm = __builtin_amdgcn_readfirstlane(tm);
   tk = __builtin_amdgcn_readfirstlane(tk);
-  const int64_t m0 = static_cast<int64_t>(tm) * kTile, k0 = static_cast<int64_t>(tk) * kTile;
+  const int64_t m0 = static_cast<int64_t>(tm) * kRows, k0 = static_cast<int64_t>(tk) * kTile;
   const int64_t nbr = K / 64;
   const int64_t nsteps = cdiv(N, 64), npairs = (nsteps + 1) / 2;
   const int64_t st0 = kMulti ? 2 * (npairs * split / ml.S) : 0;
@@ -680,22 +683,22 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   // read as zero without a branch. (Columns past N in the last step read the
   // next row; the matching weight rows are dead, so they contribute zero.)
   const int ach = t & 7, arow0 = t >> 3;
-  const int64_t rows_valid = imin(static_cast<int64_t>(kTile), M - m0);
+  const int64_t rows_valid = imin(static_cast<int64_t>(kRows), M - m0);
   const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(dy + m0 * N), 0, static_cast<int>(rows_valid * N * 2), kBufferDword3);
-  uint32_t aoff[4];
+  uint32_t aoff[MB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) aoff[i] = static_cast<uint32_t>((arow0 + 64 * i) * N * 2 + 16 * ach);
-  u32x4 areg[4];
+  for (int i = 0; i < MB; ++i) aoff[i] = static_cast<uint32_t>((arow0 + 64 * i) * N * 2 + 16 * ach);
+  u32x4 areg[MB];
   auto load_a = [&](int64_t st) {
     const uint32_t so = static_cast<uint32_t>(imin(st, nsteps - 1) * 128);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MB; ++i)
       areg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(yr, aoff[i], so, 0));
   };
   auto store_a = [&](u32x4* Ab) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Ab[a_slot(arow0 + 64 * i, ach)] = areg[i];
+    for (int i = 0; i < MB; ++i) Ab[a_slot(arow0 + 64 * i, ach)] = areg[i];
   };
   // this thread decodes half bh = t >> 8 (columns 32 bh .. 32 bh + 31) of
   // 64-column block t & 3 of weight row (t >> 2) & 63 of the step
@@ -716,9 +719,9 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   // and a transposed read phase (4 rows x 4 aligned chunks of one block) still does.
   auto w_slot = [](int row, int c) { return row * kBwRow + (c ^ ((c >> 3) & 3)); };
 
-  f32x16 acc[4][2];
+  f32x16 acc[MB][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -743,10 +746,10 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
 #pragma unroll
     for (int j = 0; j < 2; ++j) bf[j] = read_bj(Wb, s, j);
   };
-  auto read_a = [&](const u32x4* Ab, int s, bf16x8 (&af)[4]) {
-    const int sw = (2 * s + h) ^ a_swz(l32);       // a_swz(128 wm + 32 i + l32) == a_swz(l32)
+  auto read_a = [&](const u32x4* Ab, int s, bf16x8 (&af)[MB]) {
+    const int sw = (2 * s + h) ^ a_swz(l32);       // a_swz(32 (MB wm + i) + l32) == a_swz(l32)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) af[i] = as_bf16x8(Ab[(128 * wm + 32 * i + l32) * 8 + sw]);
+    for (int i = 0; i < MB; ++i) af[i] = as_bf16x8(Ab[(32 * (MB * wm + i) + l32) * 8 + sw]);
   };
 
   // one step: MFMAs on (Ab, Wb); decode `nx` into Wn; load dY tile st+1 and
@@ -759,7 +762,7 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
     __builtin_amdgcn_sched_barrier(0);
     const MagTable tb = make_table(cb, block_scale(nx.q, nx.d) * nx.live);
     const uint32_t pw[4] = {nx.p.x, nx.p.y, nx.p.z, nx.p.w};
-    bf16x8 af[2][4], bf[2][2];
+    bf16x8 af[2][MB], bf[2][2];
     read_a(Ab, 0, af[0]);
     read_b(Wb, 0, bf[0]);
     __builtin_amdgcn_sched_barrier(0);
@@ -774,19 +777,19 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
         read_b(Wb, s + 1, bf[(s + 1) & 1]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(af[s & 1][i], bf[s & 1][j], acc[i][j]);
       Wn[w_slot(brow, 8 * bkb + 4 * bh + s)] = decode8(pw[s], tb);
       if (s == 3) store_a(An);
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
+      for (int m = 0; m < 2 * MB; ++m) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (s < 3) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+        if (s < 3) __builtin_amdgcn_sched_group_barrier(0x100, MB == 4 ? 1 : MB == 2 ? 2 : 3, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 12 / MB, 0);
       }
       if (s == 3)
-        __builtin_amdgcn_sched_group_barrier(0x200, 5, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1 + MB, 0);
       else
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
       __builtin_amdgcn_sched_barrier(0);
@@ -795,7 +798,7 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
 
   // a pool's rows: asked for here, used in the epilogue
   TileRows tr;
-  if constexpr (kMulti) tr.init(ml, m0, M, lane);
+  if constexpr (kMulti) tr.init(ml, m0, M < m0 + kRows ? M : m0 + kRows, lane);
 
   // prologue: dY tile 0, codes of steps 0 and 1; decode step 0
   BCodes P0, P1;
@@ -896,15 +899,15 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
       for (int q = 0; q < 4; ++q) pend[q] = __ballot(tr.id[q] >= 0);
       // u of the wave's rows once, where it fits the registers
       constexpr bool kKeep = RS <= 2;
-      u32x4 uf[kKeep ? 4 : 1][RS];
+      u32x4 uf[kKeep ? MB : 1][RS];
       auto load_u = [&](int i, u32x4 (&f)[RS]) {
-        const int64_t mrow = imin(m0 + 128 * wm + 32 * i + l32, M - 1);
+        const int64_t mrow = imin(m0 + 32 * (MB * wm + i) + l32, M - 1);
 #pragma unroll
         for (int rs = 0; rs < RS; ++rs) f[rs] = ld16(ul + mrow * rp + 16 * rs + 8 * h);
       };
       if constexpr (kKeep) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_u(i, uf[i]);
+        for (int i = 0; i < MB; ++i) load_u(i, uf[i]);
       }
       for (int ord = 0; pend[0] | pend[1] | pend[2] | pend[3]; ++ord) {
         const int a = pend[0]   ? __builtin_amdgcn_readlane(tr.id[0], __builtin_ctzll(pend[0]))
@@ -921,10 +924,11 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
         __syncthreads();                       // the reads of the slice before (or of the last W' tile)
         stage_a(Al + static_cast<int64_t>(a) * r * K);
         __syncthreads();
-        const uint64_t r0 = wm ? rows[2] : rows[0], r1 = wm ? rows[3] : rows[1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t rm = static_cast<uint32_t>((i < 2 ? r0 : r1) >> (32 * (i & 1)));
+        for (int i = 0; i < MB; ++i) {
+          // block MB wm + i of the tile
+          const uint64_t two = rows[i >> 1], two1 = rows[(MB + i) >> 1];
+          const uint32_t rm = static_cast<uint32_t>(wm ? two1 >> (32 * ((MB + i) & 1)) : two >> (32 * (i & 1)));
           if constexpr (!kKeep) load_u(i, uf[0]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -952,23 +956,23 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   }
   if constexpr (kMulti) {
     if (ml.S > 1) {
-      float* const pt = ml.part + (split * M + m0 + 128 * wm) * K + k0 + 64 * wn + l32;
+      float* const pt = ml.part + (split * M + m0 + 32 * MB * wm) * K + k0 + 64 * wn + l32;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
             const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-            if (m0 + 128 * wm + row < M && k0 + 64 * wn + 32 * j + l32 < K) pt[row * K + 32 * j] = acc[i][j][v];
+            if (m0 + 32 * MB * wm + row < M && k0 + 64 * wn + 32 * j + l32 < K) pt[row * K + 32 * j] = acc[i][j][v];
           }
       return;
     }
   }
-  if (m0 + kTile <= M && k0 + kTile <= K) {
-    uint16_t* dt = dx + (m0 + 128 * wm + 4 * h) * K + k0 + 64 * wn + l32;
+  if (m0 + kRows <= M && k0 + kTile <= K) {
+    uint16_t* dt = dx + (m0 + 32 * MB * wm + 4 * h) * K + k0 + 64 * wn + l32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -976,13 +980,13 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
           dt[(32 * i + 8 * (v >> 2) + (v & 3)) * K + 32 * j] = bf16_bits(acc[i][j][v]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t kk = k0 + 64 * wn + 32 * j + l32;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const int64_t mm = m0 + 128 * wm + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+          const int64_t mm = m0 + 32 * (MB * wm + i) + 8 * (v >> 2) + 4 * h + (v & 3);
           if (mm < M && kk < K) dx[mm * K + kk] = bf16_bits(acc[i][j][v]);
         }
       }
@@ -1164,33 +1168,41 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
 
 // How a call of op 0 (forward, contraction over K) or 1 (backward, over N) runs.
 // The contraction of the tiled kernels is split while the tiles leave CUs
-// idle: into S ranges of at least two super-steps (forward, 256 deep) or eight
-// steps (backward, 64 deep). The time of each way, in us, from the shapes
-// measured:
-//   tiled      ranges of 64-deep steps at 1.4 each, 8 to start and end, and the
-//              partial sums written and read at 4 TB/s and another launch
+// idle, into S ranges of at least two super-steps (forward, 256 deep) or 2 MB
+// steps (backward, 64 deep); the backward's tile has 256, 128 or 64 rows (MB 4,
+// 2, 1). The time of each way, in us, from the shapes measured:
+//   tiled      ranges of 64-deep steps (forward 1.4 each; backward 1.3, 0.75,
+//              0.55 by tile), 8 to start and end, and the partial sums written and
+//              read at 4 TB/s and another launch
 //   streaming  rounds of items; an item is 9 and 2.8 per super-step of a wave
-// e.g. 700 rows at 4096 x 11008: streaming 127 (3 rounds), tiled in five ranges
-// 88; 256 rows at 4096 x 4096: streaming 24, tiled 38.
+// e.g. forward, 700 rows at 4096 x 11008: streaming 127 (3 rounds), tiled in five
+// ranges 88; 256 rows at 4096 x 4096: streaming 24, tiled 38. Backward at 4096 x
+// 4096, tiles of 256 / 128 / 64 rows at their best S: 64 rows 28.5 / 23.5 / 21.4,
+// 321 rows 35.6 / 32.1 / 98.
 struct MultiPlan {
   bool one = false, stream = false;
+  int MB = 4;                                   // backward: 32-row blocks per wave, 64 MB rows per tile
   int64_t S = 1;
   size_t t_off = 0, down_off = 0, part_off = 0, total = 0;   // the tiled kernels' workspace
 };
 static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int n) {
   MultiPlan p;
   const int64_t Kc = op == 0 ? K : N, cols = op == 0 ? N : K;
-  const int64_t tiles = cdiv(M, kTile) * cdiv(cols, kTile), steps = cdiv(Kc, 64);
+  const int64_t steps = cdiv(Kc, 64);
   if (op == 0 && M <= kMoMaxM) {
     p.one = true;
     p.total = kWsCounterBytes + mo_plan(M, N, K).part_bytes;
     return p;
   }
   double best = 0;
-  for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 8)); ++S) {
-    double us = static_cast<double>(cdiv(S * tiles, 256)) * (1.4 * 4 * cdiv(cdiv(steps, 4), S) + 8);
-    if (S > 1) us += 4 + 8e-6 * static_cast<double>(S * M * cols) / 4;
-    if (S == 1 || us < best) best = us, p.S = S;
+  for (int MB = 4; MB >= (op == 0 ? 4 : 1); MB /= 2) {
+    const int64_t tiles = cdiv(M, 64 * MB) * cdiv(cols, kTile);
+    const double step_us = op == 0 ? 1.4 : MB == 4 ? 1.3 : MB == 2 ? 0.75 : 0.55;
+    for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 2 * MB)); ++S) {
+      double us = static_cast<double>(cdiv(S * tiles, 256)) * (step_us * 4 * cdiv(cdiv(steps, 4), S) + 8);
+      if (S > 1) us += 4 + 8e-6 * static_cast<double>(S * M * cols) / 4;
+      if (best == 0 || us < best) best = us, p.S = S, p.MB = MB;
+    }
   }
   if (op == 0 && M <= kMsMaxM) {
     const MsPlan m = ms_plan(M, N, K, r, n);
@@ -1283,10 +1295,16 @@ hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K,
                                          stream);
   if (e != hipSuccess) return e;
   const int rp = static_cast<int>(rank_pad(r));
-  const dim3 grid(static_cast<unsigned>(cdiv(M, kTile) * cdiv(K, kTile) * p.S));
-#define QNF4_MBWD(RSNV)                                                                                       \
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_bwd<RSNV, true>), grid, dim3(kBwThreads), 0, stream, dy, M, N, K, packed, \
+  const dim3 grid(static_cast<unsigned>(cdiv(M, 64 * p.MB) * cdiv(K, kTile) * p.S));
+#define QNF4_MBWD1(RSNV, MBV)                                                                                 \
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(k_gemm_bwd<RSNV, true, MBV>), grid, dim3(kBwThreads), 0, stream, dy, M, N, K, packed, \
                      qscale, step, static_cast<const uint16_t*>(ul), rp, A, r, 0.0f, dx, cb, ml)
+#define QNF4_MBWD(RSNV)                     \
+  do {                                      \
+    if (p.MB == 4) QNF4_MBWD1(RSNV, 4);     \
+    else if (p.MB == 2) QNF4_MBWD1(RSNV, 2); \
+    else QNF4_MBWD1(RSNV, 1);               \
+  } while (0)
   mark_kernel(0, stream);
   switch (r <= 16 ? 1 : rp / 16) {
     case 1: QNF4_MBWD(1); break;
@@ -1296,6 +1314,7 @@ hipError_t launch_multi_bwd(const uint16_t* dy, int64_t M, int64_t N, int64_t K,
     default: QNF4_MBWD(8); break;
   }
 #undef QNF4_MBWD
+#undef QNF4_MBWD1
   mark_kernel(1, stream);
   return launch_split_sum(ml, M * K, dx, stream);
 }

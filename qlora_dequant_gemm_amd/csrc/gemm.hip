@@ -1178,7 +1178,8 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
 // e.g. forward, 700 rows at 4096 x 11008: streaming 127 (3 rounds), tiled in five
 // ranges 88; 256 rows at 4096 x 4096: streaming 24, tiled 38. Backward at 4096 x
 // 4096, tiles of 256 / 128 / 64 rows at their best S: 64 rows 28.5 / 23.5 / 21.4,
-// 321 rows 35.6 / 32.1 / 98.
+// 128 rows 32.8 / 25.2 / 25.5, 321 rows 35.6 / 32.1 / 98, 600 rows 47 / 60 / 100:
+// hence 64-row tiles up to 64 rows, 128-row ones up to 384.
 struct MultiPlan {
   bool one = false, stream = false;
   int MB = 4;                                   // backward: 32-row blocks per wave, 64 MB rows per tile
@@ -1194,15 +1195,14 @@ static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int 
     p.total = kWsCounterBytes + mo_plan(M, N, K).part_bytes;
     return p;
   }
+  p.MB = op == 0 || M > 384 ? 4 : M > 64 ? 2 : 1;
+  const int64_t tiles = cdiv(M, 64 * p.MB) * cdiv(cols, kTile);
+  const double step_us = op == 0 ? 1.4 : p.MB == 4 ? 1.3 : p.MB == 2 ? 0.75 : 0.55;
   double best = 0;
-  for (int MB = 4; MB >= (op == 0 ? 4 : 1); MB /= 2) {
-    const int64_t tiles = cdiv(M, 64 * MB) * cdiv(cols, kTile);
-    const double step_us = op == 0 ? 1.4 : MB == 4 ? 1.3 : MB == 2 ? 0.75 : 0.55;
-    for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 2 * MB)); ++S) {
-      double us = static_cast<double>(cdiv(S * tiles, 256)) * (step_us * 4 * cdiv(cdiv(steps, 4), S) + 8);
-      if (S > 1) us += 4 + 8e-6 * static_cast<double>(S * M * cols) / 4;
-      if (best == 0 || us < best) best = us, p.S = S, p.MB = MB;
-    }
+  for (int64_t S = 1; S <= kMultiMaxSplit && (S == 1 || (S * tiles <= 256 && steps / S >= 2 * p.MB)); ++S) {
+    double us = static_cast<double>(cdiv(S * tiles, 256)) * (step_us * 4 * cdiv(cdiv(steps, 4), S) + 8);
+    if (S > 1) us += 4 + 8e-6 * static_cast<double>(S * M * cols) / 4;
+    if (S == 1 || us < best) best = us, p.S = S;
   }
   if (op == 0 && M <= kMsMaxM) {
     const MsPlan m = ms_plan(M, N, K, r, n);

@@ -369,7 +369,7 @@ int qlora_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M,
  *           neighbours are faster.
  * A NaN or infinity in one adapter, its scale or a row reaches only the rows
  * (or the gradients) that use it. Every pointer is 16-byte aligned except scale
- * and index (4 bytes). M < 2^31; sizes otherwise as in qlora_nf4_lora_fwd.
+ * and index (4 bytes). M < 2^28; sizes otherwise as in qlora_nf4_lora_fwd.
  *
  * qlora_nf4_lora_fwd_multi:  y_m  = bf16( x_m . W'^T + t_m . B_a^T ),
  *                            t_m  = bf16(s_a . x_m . A_a^T),  a = index[m]
@@ -421,7 +421,7 @@ size_t qlora_workspace_bytes_multi(int op, int64_t M, int64_t N, int64_t K,
  * state for the adapters alone, the kept activations are what is left of a
  * step's memory ("A 65B fine-tune on the GPU you already have", figure 1;
  * "QLoRA Explained", "What is QLoRA?").
- *   x       [numel] bf16, numel > 0 a multiple of 64 (a layer input [M, K], K a
+ *   x       [numel] bf16, 0 < numel < 2^37 a multiple of 64 (a layer input [M, K], K a
  *           multiple of 64, in row-major order).
  *   fmt     QLORA_ACT_INT8: code = rne(127 x / top), signed bytes;
  *           QLORA_ACT_E4M3: code = the OCP e4m3 value nearest 448 x / top, as

@@ -403,12 +403,12 @@ int check_pool(const uint16_t* A, const uint16_t* B, const float* scale, int n, 
   return QLORA_OK;
 }
 
-// rows are numbered with 32 bits in the lists of the gradients and in the
-// grids of the down-projections
+// rows are numbered with 32 bits in the lists of the gradients; a grid has less
+// than 2^32 threads, four and more of them a row
 int check_mm_multi(int64_t M, int64_t N, int64_t K, bool rows_of_8) {
   const int st = check_mm(M, N, K);
   if (st) return st;
-  if (M >= (int64_t{1} << 31) || (rows_of_8 && N % 8 != 0)) return QLORA_ERR_SHAPE;
+  if (M >= (int64_t{1} << 28) || (rows_of_8 && N % 8 != 0)) return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
 
@@ -504,7 +504,7 @@ int qlora_lora_grad_act8(const uint8_t* codes, const uint16_t* absmax, int fmt, 
 int qlora_act8_pack(const uint16_t* x, int64_t numel, int fmt, uint8_t* codes, uint16_t* absmax, void* stream) {
   if (!x || !codes || !absmax) return QLORA_ERR_NULL;
   if (fmt != QLORA_ACT_INT8 && fmt != QLORA_ACT_E4M3) return QLORA_ERR_DTYPE;
-  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel / 8 / 256 >= (int64_t{1} << 31)) return QLORA_ERR_SHAPE;
+  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel >= (int64_t{1} << 37)) return QLORA_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(absmax)) return QLORA_ERR_ALIGN;
   return hip_status(qnf4::launch_act8_pack(x, numel, fmt, codes, absmax, as_stream(stream)));
 }
@@ -513,7 +513,7 @@ int qlora_act8_unpack(const uint8_t* codes, const uint16_t* absmax, int64_t nume
                       void* stream) {
   if (!codes || !absmax || !out) return QLORA_ERR_NULL;
   if (fmt != QLORA_ACT_INT8 && fmt != QLORA_ACT_E4M3) return QLORA_ERR_DTYPE;
-  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel / 8 / 256 >= (int64_t{1} << 31)) return QLORA_ERR_SHAPE;
+  if (numel <= 0 || numel % QLORA_BLOCK != 0 || numel >= (int64_t{1} << 37)) return QLORA_ERR_SHAPE;
   if (!aligned16(codes) || !aligned16(absmax) || !aligned16(out)) return QLORA_ERR_ALIGN;
   return hip_status(qnf4::launch_act8_unpack(codes, absmax, numel, fmt, out, as_stream(stream)));
 }

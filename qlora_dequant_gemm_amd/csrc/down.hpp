@@ -14,6 +14,16 @@ namespace qnf4 {
 
 constexpr int kMdWaves = 4;
 
+// what a rounding leaves of v; nothing once it is infinite (inf - inf would
+// turn an infinity into a NaN)
+__device__ __forceinline__ float rest_of(float v, float rounded) {
+  const float d = v - rounded;
+  return __builtin_fabsf(d) < __builtin_inff() ? d : 0.f;
+}
+__device__ __forceinline__ f32x4 rest_of(const f32x4& v, const f32x4& rounded) {
+  return f32x4{rest_of(v[0], rounded[0]), rest_of(v[1], rounded[1]), rest_of(v[2], rounded[2]), rest_of(v[3], rounded[3])};
+}
+
 // A wave takes at most four rank tiles of 16 (its registers), so the four waves
 // are (4 / groups) shares of the contraction x groups of rank tiles.
 template <int RT>
@@ -48,8 +58,9 @@ constexpr int md_lds() {
 }
 
 // This wave's share of the product of 16 RM rows of `in` with the adapter W
-// (kBT: B [Kc][r], else A [r][Kc]) over the 64-deep chunks [qb, qe): its share's of them Lane (g, c) supplies 16 elements at 16 g of each chunk of
-// row rows[i] of tile i. XF: the format of `in` (kActBf16, or a checkpoint with
+// (kBT: B [Kc][r], else A [r][Kc]) over its share of the 64-deep chunks [qb,
+// qe). Lane (g, c) supplies 16 elements at 16 g of each chunk of row rows[i] of
+// tile i. XF: the format of `in` (kActBf16, or a checkpoint with
 // one constant per 64 values in `tops`). An absent row (< 0) repeats row 0 and a
 // rank past r repeats the first piece: they end in sums that nobody takes.
 // Columns past Kc (Kc % 64 != 0) are cleared on both sides. kVec: the rows of B

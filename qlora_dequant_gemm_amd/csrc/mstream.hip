@@ -6,7 +6,7 @@
 // tiles would leave most of the chip idle, so the weight is streamed by small
 // items.
 //
-// k_mprep (one launch before it): t of every row, and x copied into the order
+// k_mdown (one launch before it): t of every row, and x copied into the order
 // in which the MFMAs take it (16 rows x 256 deep = eight 1 KB fragments), rows
 // past M and columns past K zero. The main kernel's loads of x are then whole
 // 1 KB lines from L2 straight into registers: no LDS, no barrier in its loop.
@@ -464,8 +464,10 @@ __global__ __launch_bounds__(256, 2) void k_mone(MoArgs P, MultiLora ml, Codeboo
         v[e] = a;
       }
       hi = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-      lo = u32x4{pack_bf16x2(v[0] - bf16_lo(hi.x), v[1] - bf16_hi(hi.x)), pack_bf16x2(v[2] - bf16_lo(hi.y), v[3] - bf16_hi(hi.y)),
-                 pack_bf16x2(v[4] - bf16_lo(hi.z), v[5] - bf16_hi(hi.z)), pack_bf16x2(v[6] - bf16_lo(hi.w), v[7] - bf16_hi(hi.w))};
+      auto low = [&](int e, uint32_t h) {
+        return pack_bf16x2(rest_of(v[e], bf16_lo(h)), rest_of(v[e + 1], bf16_hi(h)));
+      };
+      lo = u32x4{low(0, hi.x), low(2, hi.y), low(4, hi.z), low(6, hi.w)};
     });
   }
   if (P.S > 1) {

@@ -369,7 +369,7 @@ __device__ __forceinline__ void put_split(uint16_t* qt, int64_t chunk, int row, 
     b.x = pack_bf16x2(v[0], v[1]);
     b.y = pack_bf16x2(v[2], v[3]);
     *reinterpret_cast<u32x2*>(qt + ((chunk * kSplit + k) * 16 * RT + j) * 64 + row) = b;
-    v -= f32x4{bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)};
+    v = rest_of(v, f32x4{bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)});
   }
 }
 
@@ -869,13 +869,14 @@ MultiGradPlan multi_grad_plan(int64_t M, int64_t N, int64_t K, int r, int n, boo
   // t and u: about one workgroup per CU (more splits cost more than they
   // hide: 4096 rows at 11008 x 4096 29 us with 4, 43 with 14), each chunk's split between them by
   // their lengths, two 64-deep pieces and more per wave (513 rows, 4096 deep:
-  // 12.5 us in 16 ranges, 10.9 in 8, 11.3 in 4)
-  const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(288 / g.chunks, 2);
+  // 12.5 us in 16 ranges, 10.9 in 8, 11.3 in 4). From 145 chunks on nothing is
+  // split: a split chunk needs an arrival counter, of which there are 4096.
+  const int64_t nk = cdiv(K, 64), nn = cdiv(N, 64), q = std::max<int64_t>(288 / g.chunks, 1);
   auto splits = [&](int64_t want, int64_t pieces) {
     return std::max<int64_t>(std::min({want, cdiv(pieces, 2 * kMdWaves), int64_t{kMdMaxSplit}}), 1);
   };
   g.St = splits(std::max<int64_t>((q * nk + (nk + nn) / 2) / (nk + nn), 1), nk);
-  g.Su = splits(q - std::min(q - 1, g.St), nn);
+  g.Su = splits(q > 1 ? q - std::min(q - 1, g.St) : 1, nn);
   // items: about two workgroups per CU over all column tiles; an item's
   // partial sums (4 r bytes a column) stay small beside the rows it reads (r 16,
   // 513 rows: 8.6 us with items of two chunks, 10.2 of four; r 64, 4096 rows:

@@ -458,3 +458,118 @@ def test_full_size(qops, M, N, K, r):
     assert fro(qops.bwd_dx_multi(dy, qw, pool, index), dx) < 5e-3
     dA, dB = qops.lora_grad_multi(x, dy, pool, index)
     assert fro(dA, rA) < 1e-5 and fro(dB, rB) < 1e-5
+
+
+def test_gradients_of_many_chunks(qops):
+    """More chunks (2064) than half the arrival counters, K at least three times
+    N: the last rows' adapter, the pool's and the single one's gradients, and a
+    second call on the workspace that the first one left."""
+    M, N, K, r, n = 132000, 64, 576, 8, 3
+    g = np.random.Generator(np.random.PCG64(71))
+    x = (torch.from_numpy(g.standard_normal((M, K)).astype(np.float32))).to(torch.bfloat16)
+    dy = torch.from_numpy(g.standard_normal((M, N)).astype(np.float32) * 0.1).to(torch.bfloat16)
+    A, B = bits(g.standard_normal((n, r, K)) * K ** -0.5), bits(g.standard_normal((n, N, r)) * 0.1)
+    s = np.array([1.0, 0.5, 2.0], np.float32)
+    idx = np.repeat(np.array([1, -1, 2], np.int32), [100000, 1000, M - 101000])
+    pool, ws = qops.AdapterPool(dev(A), dev(B), dev(s)), qops.Workspace("cuda")
+    for fmt in (None, "int8"):
+        xd = x.cuda() if fmt is None else qops.act8_pack(x.cuda(), fmt)
+        xv = x if fmt is None else qops.act8_unpack(xd).cpu()
+        x64, d64 = xv.double().numpy(), dy.double().numpy()
+        first = qops.lora_grad_multi(xd, dy.cuda(), pool, dev(idx), ws=ws)
+        again = qops.lora_grad_multi(xd, dy.cuda(), pool, dev(idx), ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+        single = []
+        if fmt:
+            single = [(*qops.lora_grad(xd, dy.cuda(), dev(A[2]), dev(B[2]), alpha=8.0, ws=ws), slice(0, M), 2, 1.0)]
+        got = [(first[0][a], first[1][a], idx == a, a, float(s[a])) for a in range(n)] + single
+        for dA, dB, rows, a, sc in got:
+            xr, dr, Aa, Ba = x64[rows], d64[rows], f64(A[a]), f64(B[a])
+            U, T = dr @ Ba, xr @ Aa.T
+            aU, aT = np.abs(dr) @ np.abs(Ba), np.abs(xr) @ np.abs(Aa).T
+            c = len(xr)
+            Case.bounded(dA, sc * U.T @ xr, (N + 2 * c + 16) * 2.0 ** -23 * sc * (aU.T @ np.abs(xr)), 2.0 ** -24)
+            Case.bounded(dB, sc * dr.T @ T, (K + 2 * c + 16) * 2.0 ** -23 * sc * (np.abs(dr).T @ aT), 2.0 ** -24)
+
+
+@pytest.mark.parametrize("M", [1, 4, 20, 300])
+def test_an_infinity_stays_one(qops, M):
+    """An infinite t or u gives infinities of the formula's sign, not NaN."""
+    c = Case(qops, M, 264, 320, 16, 2, "one", 31)
+    c.A[1, 3, 0] = 0x7F80                                     # +inf
+    c.x[:, 0] = 0x3F80                                        # t[3] = +inf
+    pool = qops.AdapterPool(dev(c.A), dev(c.B), dev(c.s))
+    y = host(qops.lora_fwd_multi(dev(c.x), c.qw, pool, c.index))
+    sign = np.sign(f64(c.B[1, :, 3]))
+    assert (y[:, sign != 0] == np.inf * sign[sign != 0]).all()
+    dA, dB = qops.lora_grad_multi(dev(c.x[:1]), dev(c.dy[:1]), pool, c.index[:1])
+    sign = np.sign(f64(c.dy[0]))
+    assert (host(dB[1])[sign != 0, 3] == np.inf * sign[sign != 0]).all()
+    assert torch.isfinite(dB[1][:, :3]).all() and torch.isfinite(dA).all()
+
+
+# Offsets past 2^31 elements and 2^32 bytes. Each is compared with the same rows
+# or adapters alone, whose own results the tests above pin: t and u may round
+# differently where another number of ranges adds them (2^-8 of the LoRA term,
+# which is below a fifth of the largest output here), outputs once more (2^-8).
+def near(got, ref, rel):
+    got, ref = got.float(), ref.float()
+    assert (got - ref).abs().max() <= rel * ref.abs().max(), float((got - ref).abs().max() / ref.abs().max())
+
+
+def test_offsets_of_a_large_pool(qops):
+    n, r, K, N = 2100, 128, 8192, 64
+    g = torch.Generator("cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.float32)
+    qw, qt = qops.quantize_weight(rnd(N, K) * 0.02), qops.quantize_weight(rnd(K, N) * 0.02)
+    ends = [0, n - 1]
+    wide, small = torch.zeros(n, r, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, N, r, dtype=torch.bfloat16, device="cuda")
+    wide[ends] = (rnd(2, r, K) * K ** -0.5).bfloat16()
+    small[ends] = (rnd(2, N, r) * 0.1).bfloat16()
+    scale = torch.ones(n, device="cuda")
+    pool = qops.AdapterPool(wide, small, scale)               # A past 2^31 elements
+    few = qops.AdapterPool(wide[ends].contiguous(), small[ends].contiguous(), scale[:2].contiguous())
+    turn = qops.AdapterPool(small.view(n, r, N), wide.view(n, K, r), scale)          # B past them
+    fewt = qops.AdapterPool(small[ends].view(2, r, N).contiguous(), wide[ends].view(2, K, r).contiguous(), scale[:2].contiguous())
+    for M in (3, 20, 300, 1100):
+        idx = torch.arange(M, device="cuda", dtype=torch.int32) % 2
+        big = idx * (n - 1)
+        x, dy = rnd(M, K).bfloat16(), rnd(M, N).bfloat16()
+        near(qops.lora_fwd_multi(x, qw, pool, big), qops.lora_fwd_multi(x, qw, few, idx), 2.0 ** -7)
+        near(qops.bwd_dx_multi(dy, qw, pool, big), qops.bwd_dx_multi(dy, qw, few, idx), 2.0 ** -7)
+        near(qops.lora_fwd_multi(dy, qt, turn, big), qops.lora_fwd_multi(dy, qt, fewt, idx), 2.0 ** -7)
+        near(qops.bwd_dx_multi(x, qt, turn, big), qops.bwd_dx_multi(x, qt, fewt, idx), 2.0 ** -7)
+        dA, dB = qops.lora_grad_multi(x, dy, pool, big)       # dA 8.8 GB
+        fA, fB = qops.lora_grad_multi(x, dy, few, idx)
+        near(dA[ends], fA, 2.0 ** -18)
+        near(dB[ends], fB, 2.0 ** -18)
+        assert not dA[1:-1].any() and not dB[1:-1].any()
+        del dA, dB
+
+
+def test_offsets_of_a_large_batch(qops):
+    M, K, N, r, n, tail = 270000, 8192, 64, 16, 3, 300
+    g = torch.Generator("cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.float32)
+    qw, qt = qops.quantize_weight(rnd(N, K) * 0.02), qops.quantize_weight(rnd(K, N) * 0.02)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)        # 4.4 GB
+    dy = torch.randn((M, N), generator=g, device="cuda", dtype=torch.bfloat16)
+    A, B = (rnd(n, r, K) * K ** -0.5).bfloat16(), (rnd(n, N, r) * 0.1).bfloat16()
+    scale = torch.ones(n, device="cuda")
+    pool = qops.AdapterPool(A, B, scale)
+    turn = qops.AdapterPool(B.view(n, r, N), A.view(n, K, r), scale)
+    idx = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    idx[-tail:] = (torch.arange(tail, device="cuda") // 64 % n).int()
+    xt, dt, it = x[-tail:], dy[-tail:], idx[-tail:].contiguous()
+    near(qops.lora_fwd_multi(x, qw, pool, idx)[-tail:], qops.lora_fwd_multi(xt, qw, pool, it), 2.0 ** -7)
+    near(qops.bwd_dx_multi(x, qt, turn, idx)[-tail:], qops.bwd_dx_multi(xt, qt, turn, it), 2.0 ** -7)
+    near(qops.lora_fwd_multi(dy, qt, turn, idx)[-tail:], qops.lora_fwd_multi(dt, qt, turn, it), 2.0 ** -7)   # y 4.4 GB
+    near(qops.bwd_dx_multi(dy, qw, pool, idx)[-tail:], qops.bwd_dx_multi(dt, qw, pool, it), 2.0 ** -7)
+    for a, b in zip(qops.lora_grad_multi(x, dy, pool, idx), qops.lora_grad_multi(xt, dt, pool, it)):
+        near(a, b, 2.0 ** -18)
+    kept, small = qops.act8_pack(x, "e4m3"), qops.act8_pack(xt, "e4m3")
+    assert torch.equal(kept.codes[-tail:], small.codes)
+    assert torch.equal(kept.absmax[-tail * K // 64:].view(torch.int16), small.absmax.view(torch.int16))
+    assert torch.equal(qops.act8_unpack(kept)[-tail:], qops.act8_unpack(small))
+    for a, b in zip(qops.lora_grad_multi(kept, dy, pool, idx), qops.lora_grad_multi(small, dt, pool, it)):
+        near(a, b, 2.0 ** -18)

@@ -164,3 +164,23 @@ def test_workspace_query():
     assert q(2, 4096, 4096, 4096, 16, 4096) < 8 * q(2, 4096, 4096, 4096, 16, 1)
     for op in range(4):
         assert q(op, 333, 136, 320, 24, 5) % 256 == 0
+
+
+def test_gradients_of_long_batches_split_nothing():
+    """A split product of a chunk needs one of 4096 arrival counters, so a batch
+    of more than 2048 chunks has none: its workspace holds the rows' lists, t and
+    u, and the items' sums, and no partial sums of t and u (130 KB a chunk)."""
+    M, K, N, r = 132000, 576, 64, 8
+    chunks = M // 64 + 2
+    items = 2 * (M // 64) * 4 * 256 * 16 * 4 // 17
+    need = _lib.lib().qlora_workspace_bytes_multi(2, M, N, K, r, 2)
+    assert 0 < need < 16384 + chunks * 64 * (4 + 2 * 3 * 16 * 2) + items + (1 << 20)
+    assert 0 < _lib.lib().qlora_workspace_bytes_multi(3, M, N, K, r, 1) < need + (1 << 20)
+
+
+def test_limits_of_rows_and_values():
+    size = _lib.lib().qlora_workspace_bytes_multi
+    for op in range(4):
+        assert size(op, (1 << 28) - 1, 8, 64, 1, 1) > 0 and size(op, 1 << 28, 8, 64, 1, 1) == 0
+    P, U = _lib.lib().qlora_act8_pack, _lib.lib().qlora_act8_unpack
+    assert P(FAKE, 1 << 37, 0, FAKE, FAKE, V(0)) == 2 and U(FAKE, FAKE, 1 << 37, 0, FAKE, V(0)) == 2

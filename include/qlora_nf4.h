@@ -375,10 +375,10 @@ int qlora_lora_grad(const uint16_t* x, const uint16_t* dy, int64_t M,
  *                            t_m  = bf16(s_a . x_m . A_a^T),  a = index[m]
  * qlora_nf4_bwd_dx_multi:    dX_m = bf16( dY_m . W' + u_m . A_a ),
  *                            u_m  = bf16(s_a . dY_m . B_a);  N a multiple of 8
- *     For M <= 4 the forward splits K and carries each range's part of t as the
- *     sum of two bf16 numbers (about 16 significant bits), as
- *     qlora_nf4_lora_fwd does for M <= 16. Repeated identical calls are bitwise
- *     identical.
+ *     For M <= 4 and few adapter values (a rule on N, K, r, n) the forward splits
+ *     K and carries each range's part of t as the sum of two bf16 numbers (about
+ *     16 significant bits), as qlora_nf4_lora_fwd does for M <= 16. Repeated
+ *     identical calls are bitwise identical.
  * qlora_lora_grad_multi:     dB_a = s_a sum_m dY_m^T (x_m . A_a^T)   [n, N, r]
  *                            dA_a = s_a sum_m (dY_m . B_a)^T x_m     [n, r, K]
  *     over the rows m of adapter a, fp32; t and u enter as three bf16 numbers

@@ -1190,7 +1190,13 @@ static MultiPlan multi_plan(int op, int64_t M, int64_t N, int64_t K, int r, int 
   MultiPlan p;
   const int64_t Kc = op == 0 ? K : N, cols = op == 0 ? N : K;
   const int64_t steps = cdiv(Kc, 64);
-  if (op == 0 && M <= kMoMaxM) {
+  // One launch for up to four rows, while the adapters that every block of 64
+  // weight rows reads again (min(n, M) of them at most: the index is on the
+  // device) cost less than the second launch: one row r 16 / 64 at 4096 x 4096
+  // (8 / 34 MB) 11.0 / 15.2 us against 17.9 / 22.3 in two launches, r 16 at 11008 x
+  // 4096 (23 MB) 21.9 against 24.3; four rows of four adapters there (90 MB) 32.9
+  // against 24.9, at r 64 (361 MB) 75 against 30.
+  if (op == 0 && M <= kMoMaxM && cdiv(N, 64) * std::min<int64_t>(n, M) * 16 * down_nt(r) * K * 2 <= 72000000) {
     p.one = true;
     p.total = kWsCounterBytes + mo_plan(M, N, K).part_bytes;
     return p;

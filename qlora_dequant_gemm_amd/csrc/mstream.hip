@@ -301,9 +301,11 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_mstream(MsArgs P, Mult
 // joins its partial sums of y, t as two bf16 numbers (hi + lo, about 16 bits: a
 // rounding of each share to one would add S roundings), so nothing waits for
 // the whole of t. The last range of a row block to arrive adds them in order.
-// The adapter's 2 r bytes a column are read by every row block, from L2 mostly;
-// two launches (t, then k_mstream) take 17.7 us at 4096 x 4096, r 16 and one
-// row, this one 11.
+// The adapters' 2 r bytes a column are read by every row block, from L2 mostly
+// (about 6 TB/s: k_mone where they are few, see multi_plan). Two launches (t,
+// then k_mstream) take 17.9 us at 4096 x 4096, r 16 and one row, this one 11.0.
+// What bounds it there: a chain of one load from HBM, the products, a partial
+// sum and an arrival (the base alone takes 8.1).
 // ---------------------------------------------------------------------------
 struct MoArgs {
   const uint16_t* x;        // [M][K]
@@ -523,8 +525,8 @@ MoPlan mo_plan(int64_t M, int64_t N, int64_t K) {
   MoPlan p;
   const int64_t nss = cdiv(K, 256);
   p.blocks = cdiv(N, kMsRows);
-  // as ms_plan
-  p.S = std::max<int64_t>(std::min({256 / p.blocks, cdiv(nss, 4), int64_t{kMsMaxSplit}}), 1);
+  // as ms_plan, with two items per CU (11008 x 4096: 22.3 us in one range, 21.5 in two)
+  p.S = std::max<int64_t>(std::min({512 / p.blocks, cdiv(nss, 4), int64_t{kMsMaxSplit}}), 1);
   if (p.S > 1) p.part_bytes = static_cast<size_t>(p.blocks * p.S) * 4096;
   return p;
 }

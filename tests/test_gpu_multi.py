@@ -167,7 +167,8 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(40, 37, 128, 8, 3, "runs"), (260, 301, 320, 12, 3, "mixed"),
+@pytest.mark.parametrize("M,N,K,r,n,kind", SHAPES + [(4, 2056, 4160, 128, 5, "mixed"),
+                                                          (4, 4096, 1024, 16, 4, "mixed"), (40, 37, 128, 8, 3, "runs"), (260, 301, 320, 12, 3, "mixed"),
                                                      (5, 1, 2112, 16, 2, "mixed"), (48, 200, 4160, 16, 30, "mixed"),
                                                      # a contraction split over workgroups: the tiled kernel, ragged and whole
                                                      (1100, 264, 2112, 16, 6, "runs"), (1030, 520, 2048, 40, 40, "mixed"),

@@ -686,7 +686,8 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   // t & 7 of rows (t >> 3) + 64 i: eight lanes cover a row's 128 bytes.
   // Buffer loads through a descriptor over this tile's dY rows: rows past M
   // read as zero without a branch. (Columns past N in the last step read the
-  // next row; the matching weight rows are dead, so they contribute zero.)
+  // next row; the matching weight rows are dead, so they contribute zero, except
+  // with a pool, below.)
   const int ach = t & 7, arow0 = t >> 3;
   const int64_t rows_valid = imin(static_cast<int64_t>(kRows), M - m0);
   const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc(
@@ -697,9 +698,12 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   u32x4 areg[MB];
   auto load_a = [&](int64_t st) {
     const uint32_t so = static_cast<uint32_t>(imin(st, nsteps - 1) * 128);
+    // a pool's rows are kept apart: columns past N read as zero (out of range),
+    // or a NaN at the start of the next row would meet the zero weights
+    const uint32_t dead = kMulti && imin(st, nsteps - 1) * 64 + 8 * ach >= N ? 0x80000000u : 0u;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
-      areg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(yr, aoff[i], so, 0));
+      areg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(yr, aoff[i] | dead, so, 0));
   };
   auto store_a = [&](u32x4* Ab) {
 #pragma unroll

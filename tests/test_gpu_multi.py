@@ -327,6 +327,25 @@ def test_bad_numbers_stay_with_their_rows(qops, M):
     assert not torch.isfinite(dA[3]).all() and torch.isfinite(dA[0]).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(4, 264, 320), (40, 264, 320), (300, 72, 320), (300, 264, 2112), (700, 1032, 576), (1100, 264, 320)])
+def test_bad_rows_stay_apart(qops, M, N, K):
+    """Rows of NaN in x or dY change no bit of their neighbours, whose products end
+    inside a step of the contraction, nor of other adapters' gradients."""
+    c = Case(qops, M, N, K, 16, 4, "mixed", 23)
+    bad = np.arange(M) % 5 == 2
+    c.idx[bad], c.idx[~bad] = 3, c.idx[~bad] % 3
+    index, fine = dev(c.idx), torch.from_numpy(~bad).cuda()
+    res = []
+    for v in (0, 0x7FC0):
+        c.x[bad], c.dy[bad] = v, v
+        x, dy = dev(c.x), dev(c.dy)
+        dA, dB = qops.lora_grad_multi(x, dy, c.pool, index)
+        res.append((qops.lora_fwd_multi(x, c.qw, c.pool, index)[fine], qops.bwd_dx_multi(dy, c.qw, c.pool, index)[fine],
+                    dA[:3], dB[:3]))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 def test_outputs_end_where_they_end(qops):
     """Nothing is written past the outputs; a workspace full of NaN changes nothing."""
     c = Case(qops, 83, 136, 320, 24, 3, "runs", 31)

@@ -695,12 +695,13 @@ __global__ __launch_bounds__(kBwThreads, 1) void k_gemm_bwd(const uint16_t* __re
   uint32_t aoff[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) aoff[i] = static_cast<uint32_t>((arow0 + 64 * i) * N * 2 + 16 * ach);
+  const int alive = static_cast<int>(2 * N) - 16 * ach;      // bytes of a row from this thread's first chunk
   u32x4 areg[MB];
   auto load_a = [&](int64_t st) {
     const uint32_t so = static_cast<uint32_t>(imin(st, nsteps - 1) * 128);
     // a pool's rows are kept apart: columns past N read as zero (out of range),
     // or a NaN at the start of the next row would meet the zero weights
-    const uint32_t dead = kMulti && imin(st, nsteps - 1) * 64 + 8 * ach >= N ? 0x80000000u : 0u;
+    const uint32_t dead = kMulti && static_cast<int>(so) >= alive ? 0x80000000u : 0u;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
       areg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(yr, aoff[i] | dead, so, 0));
